@@ -40,7 +40,7 @@
  * state. Calls enqueue work on `stream` (a cudaStream_t; NULL = legacy
  * default stream) and return without synchronising: SRFTQ_OK means
  * "launched". A call with zero vectors launches nothing. Every other
- * successful call launches exactly one kernel.
+ * successful call launches exactly one kernel, the attention calls three.
  *
  * Errors: argument errors are detected on the host before anything is
  * launched and return a negative status. A launch failure returns
@@ -294,6 +294,124 @@ int srftq_dequantize_dense(const srftq_desc* desc, int64_t n_slices, int64_t n_r
                            int64_t in_slice_stride_rows, const uint16_t* operand,
                            const float* lambda, uint16_t* xhat, int64_t out_slice_stride_rows,
                            void* stream);
+
+/*
+ * Paged cache. A pool holds n_pages * page_size rows of codes and scales, laid
+ * out as everywhere above ([rows][H][d*bits/8] uint8, [rows][H][d/group]
+ * fp16); page p is its rows p*page_size .. (p + 1)*page_size - 1. A sequence's
+ * block table lists its pages in order: token t lies in row
+ * table[t / page_size]*page_size + t % page_size, its slot. Any page_size from
+ * 1 to 65536. The paged calls take d in {64, 128, 256} and groups of 16 or
+ * more. Integer arrays (lengths, tables, slots) need the alignment of their
+ * element only; lengths and positions stay below 2^31.
+ */
+
+/*
+ * srftq_block_tables -- the block tables and slot map of a step, from the
+ * requests' lengths. Sequence b holds max(cached_lens[b], 0) tokens and gets
+ * max(new_lens[b], 0) more. The pages that those need beyond the ones it has
+ * (ceil(cached / page_size)) are taken from free_pages in order, sequence 0
+ * first, and written behind the ones it has; all other entries of the table
+ * are left as they were. The new tokens are numbered through the batch:
+ * row_start[b] is the first of sequence b, row_start[n_seq] their number.
+ *
+ *   free_pages  int32 [n_free]            page numbers, used from the front
+ *   block_table int32 [n_seq][max_pages]  read (partly filled pages), written
+ *   slots       int64 [n_slots]           slot of each new token; -1 for rows
+ *               behind the last sequence, and for tokens without a page (free
+ *               pages used up: the table's entry is -1 too; a position at or
+ *               behind max_pages*page_size). Rows from n_slots on are dropped.
+ *   seq_lens    int32 [n_seq]             cached + new, written
+ *   row_start   int32 [n_seq + 1]         written
+ *   counts      int32 [3], written        pages taken, pages wanted, new tokens
+ *
+ * One launch, nothing read back: the call can be captured, and later calls on
+ * the stream can use its outputs at once.
+ */
+int srftq_block_tables(int64_t n_seq, const int32_t* cached_lens, const int32_t* new_lens,
+                       int64_t page_size, const int32_t* free_pages, int64_t n_free,
+                       int32_t* block_table, int64_t max_pages, int64_t* slots, int64_t n_slots,
+                       int32_t* seq_lens, int32_t* row_start, int32_t* counts, void* stream);
+
+/*
+ * srftq_quantize_paged -- srftq_quantize with row r of x stored in row
+ * slots[r] of the pool, in every slice. A row whose slot is negative, or
+ * pool_rows or more, is stored nowhere. Slots that are in range must differ
+ * from one another: a row that two of them name holds parts of both.
+ *
+ *   x      [S][x_slice_stride_rows][H][d] fp16
+ *   slots  int64 [n_rows], one map for all slices
+ *   codes  [S][pool_rows][H][d*bits/8], scales [S][pool_rows][H][d/group]
+ */
+int srftq_quantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_rows,
+                         const uint16_t* x, int64_t x_slice_stride_rows, const int8_t* signs,
+                         const float* lambda, const int64_t* slots, uint8_t* codes,
+                         uint16_t* scales, int64_t pool_rows, void* stream);
+
+/*
+ * srftq_dequantize_paged -- srftq_dequantize of the pool rows slots[r] into
+ * the rows r of xhat. A row whose slot is negative, or pool_rows or more, is
+ * left as it was; a slot may be named more than once.
+ */
+int srftq_dequantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_rows,
+                           const uint8_t* codes, const uint16_t* scales, int64_t pool_rows,
+                           const int64_t* slots, const int8_t* signs, const float* lambda,
+                           uint16_t* xhat, int64_t out_slice_stride_rows, void* stream);
+
+/* Type of the queries and outputs of srftq_prefix_attention. */
+#define SRFTQ_FP16 0
+#define SRFTQ_BF16 1
+
+/*
+ * srftq_prefix_attention -- one decode step of attention over a paged cache
+ * for a batch whose sequences share their first prefix_len tokens. For
+ * sequence b, KV head h and the query heads h*q_per_kv + j (1 <= q_per_kv <=
+ * 16), over its tokens t < len_b = clamp(seq_lens[b], 0, capacity):
+ *   out = sum_t softmax_t(softmax_scale * q . khat_t) vhat_t
+ * with khat, vhat what srftq_dequantize would return (before its fp16
+ * rounding). Token t < prefix_len is read through prefix_table, once for all
+ * sequences; token t >= prefix_len through row b of block_table (whose first
+ * entries, those of shared pages, are not read). prefix_len = 0 is plain paged
+ * decoding. capacity = max(prefix_len, max_pages*page_size).
+ *
+ * A sequence without tokens (len_b = 0, a padding row of the batch) gives
+ * zeros. A sequence may be shorter than the prefix. A token whose table entry
+ * is no page of the pool (negative, n_pages or more) is left out. What lies in
+ * the pool behind a sequence's last token is never used, whatever it holds.
+ *
+ *   q            [n_seq][heads*q_per_kv][d], out alike: fp16 or bf16 (dtype)
+ *   k_codes, v_codes, k_scales, v_scales: pools of n_pages*page_size rows
+ *   k_signs, v_signs [heads][d] int8; k_lambda, v_lambda [heads][d] float32
+ *   prefix_table int32 [ceil(prefix_len / page_size)]
+ *   block_table  int32 [n_seq][max_pages];  seq_lens int32 [n_seq]
+ *   lse_or_null  float32 [n_seq][heads*q_per_kv]: log sum_t exp(score_t), -inf
+ *                without tokens, to join this attention with another part's
+ *   workspace    at least srftq_prefix_attention_workspace() bytes, 16-byte
+ *                aligned, written; calls that may run at the same time need
+ *                one each. Nothing in it is kept from one call to the next.
+ *
+ * The parts' softmax states are kept in float32 and joined in a fixed order:
+ * the result does not depend on scheduling. Three launches, no copy to the
+ * host: lengths and tables may come from calls before it on the stream.
+ */
+int srftq_prefix_attention(const srftq_desc* desc, int32_t dtype, int64_t n_seq, int32_t q_per_kv,
+                           const void* q, const uint8_t* k_codes, const uint16_t* k_scales,
+                           const int8_t* k_signs, const float* k_lambda, const uint8_t* v_codes,
+                           const uint16_t* v_scales, const int8_t* v_signs,
+                           const float* v_lambda, int64_t n_pages, int64_t page_size,
+                           const int32_t* prefix_table, int64_t prefix_len,
+                           const int32_t* block_table, int64_t max_pages,
+                           const int32_t* seq_lens, float softmax_scale, void* out,
+                           float* lse_or_null, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
+/*
+ * srftq_prefix_attention_workspace -- bytes of workspace that a call of
+ * srftq_prefix_attention with these sizes needs on the current device, or a
+ * negative status. It follows from these sizes alone, not from the lengths.
+ */
+int64_t srftq_prefix_attention_workspace(const srftq_desc* desc, int64_t n_seq, int32_t q_per_kv,
+                                         int64_t prefix_len);
 
 /* Human-readable text for a status code (static storage, never NULL). */
 const char* srftq_status_string(int status);

@@ -36,7 +36,9 @@ SRHT = 1
 EXPORTED = ("srftq_quantize", "srftq_dequantize", "srftq_calibrate_lambda", "srftq_rotate",
             "srftq_dequantize_rotated", "srftq_unrotate", "srftq_decode_attention",
             "srftq_householder_rotation", "srftq_dense_operand", "srftq_calibrate_lambda_dense",
-            "srftq_quantize_dense", "srftq_dequantize_dense", "srftq_status_string",
+            "srftq_quantize_dense", "srftq_dequantize_dense", "srftq_block_tables",
+            "srftq_quantize_paged", "srftq_dequantize_paged", "srftq_prefix_attention",
+            "srftq_prefix_attention_workspace", "srftq_status_string",
             "srftq_check_device", "srftq_probe_wait_timeout", "srftq_probe_index_check",
             "srftq_debug_checks", "srftq_version")
 
@@ -84,6 +86,13 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.srftq_calibrate_lambda_dense.argtypes = [D, I64, I64, P, I64, P, P, P]
     lib.srftq_quantize_dense.argtypes = [D, I64, I64, P, I64, P, P, P, P, I64, P]
     lib.srftq_dequantize_dense.argtypes = [D, I64, I64, P, P, I64, P, P, P, I64, P]
+    lib.srftq_block_tables.argtypes = [I64, P, P, I64, P, I64, P, I64, P, I64, P, P, P, P]
+    lib.srftq_quantize_paged.argtypes = [D, I64, I64, P, I64, P, P, P, P, P, I64, P]
+    lib.srftq_dequantize_paged.argtypes = [D, I64, I64, P, P, I64, P, P, P, P, I64, P]
+    lib.srftq_prefix_attention.argtypes = [D, ctypes.c_int32, I64, ctypes.c_int32, P, P, P, P, P,
+                                           P, P, P, P, I64, I64, P, I64, P, I64, P,
+                                           ctypes.c_float, P, P, P, I64, P]
+    lib.srftq_prefix_attention_workspace.argtypes = [D, I64, ctypes.c_int32, I64]
     lib.srftq_status_string.argtypes = [I32]
     lib.srftq_status_string.restype = ctypes.c_char_p
     lib.srftq_check_device.argtypes = [P]
@@ -94,6 +103,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     for name in EXPORTED:
         if name != "srftq_status_string":
             getattr(lib, name).restype = I32
+    lib.srftq_prefix_attention_workspace.restype = I64
     _libs[path] = lib
     return lib
 
@@ -424,6 +434,167 @@ def srftq_dequantize_dense(desc: SrftqDesc, codes, scales, operand, lam, xhat,
     _check("srftq_dequantize_dense", st)
 
 
+def _ints(t, dtype, shape: tuple, name: str):
+    """Address of a contiguous integer tensor of the given shape."""
+    _check_tensor(t, dtype, name)
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {list(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _vector(t, dtype, name: str):
+    """(address, length) of a contiguous one-dimensional tensor."""
+    _check_tensor(t, dtype, name)
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous vector, got {tuple(t.shape)}")
+    return t.data_ptr(), t.shape[0]
+
+
+def _pool(t, S: int, H: int, row_elems: int, name: str, dtype):
+    """(address, rows) of a contiguous [S, rows, H, e] pool."""
+    _check_tensor(t, dtype, name)
+    if (t.dim() != 4 or t.shape[0] != S or t.shape[2] != H or t.shape[3] != row_elems
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected contiguous [{S}, rows, {H}, {row_elems}], "
+                         f"got {tuple(t.shape)}")
+    return t.data_ptr(), t.shape[1]
+
+
+def srftq_block_tables(cached_lens, new_lens, free_pages, block_table, page_size: int, slots,
+                       seq_lens, row_start, counts, stream=None) -> None:
+    """Block tables and slot map of a step from the requests' lengths (see
+    include/srftq.h): int32 tensors, slots int64; block_table [n_seq, max_pages]
+    is extended in place, the last four are written."""
+    import torch
+
+    lib = load_library()
+    I32, I64 = torch.int32, torch.int64
+    pc, n_seq = _vector(cached_lens, I32, "cached_lens")
+    pf, n_free = _vector(free_pages, I32, "free_pages")
+    ps, n_slots = _vector(slots, I64, "slots")
+    _check_tensor(block_table, I32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != n_seq or not block_table.is_contiguous():
+        raise ValueError(f"block_table: expected contiguous [{n_seq}, max_pages], got "
+                         f"{tuple(block_table.shape)}")
+    st = lib.srftq_block_tables(n_seq, pc, _ints(new_lens, I32, (n_seq,), "new_lens"),
+                                int(page_size), pf, n_free, block_table.data_ptr(),
+                                block_table.shape[1], ps, n_slots,
+                                _ints(seq_lens, I32, (n_seq,), "seq_lens"),
+                                _ints(row_start, I32, (n_seq + 1,), "row_start"),
+                                _ints(counts, I32, (3,), "counts"), _stream_handle(stream))
+    _check("srftq_block_tables", st)
+
+
+def srftq_quantize_paged(desc: SrftqDesc, x, signs, lam, slots, codes, scales,
+                         stream=None) -> None:
+    """x [S,N,H,d] fp16 -> rows slots[r] (int64 [N]) of the pools codes
+    [S,rows,H,d*bits/8] uint8 and scales [S,rows,H,d/G] fp16."""
+    lib = load_library()
+    F16, U8, I8, F32 = _dtypes()
+    import torch
+
+    H, d = desc.heads, desc.d
+    px, S, N, xs = _rows_view(x, H, d, "x", F16)
+    pc, rows = _pool(codes, S, H, d * desc.bits // 8, "codes", U8)
+    ps, rows2 = _pool(scales, S, H, d // desc.group, "scales", F16)
+    if rows2 != rows:
+        raise ValueError("codes and scales must have the same rows")
+    st = lib.srftq_quantize_paged(ctypes.byref(desc), S, N, px, xs,
+                                  _table(signs, S, H, d, "signs", I8),
+                                  _table(lam, S, H, d, "lambda", F32),
+                                  _ints(slots, torch.int64, (N,), "slots"), pc, ps, rows,
+                                  _stream_handle(stream))
+    _check("srftq_quantize_paged", st)
+
+
+def srftq_dequantize_paged(desc: SrftqDesc, codes, scales, slots, signs, lam, xhat,
+                           stream=None) -> None:
+    """Rows slots[r] of the pools -> rows r of xhat [S,N,H,d] fp16 (rows with a
+    negative slot are left as they were)."""
+    lib = load_library()
+    F16, U8, I8, F32 = _dtypes()
+    import torch
+
+    H, d = desc.heads, desc.d
+    px, S, N, xs = _rows_view(xhat, H, d, "xhat", F16)
+    pc, rows = _pool(codes, S, H, d * desc.bits // 8, "codes", U8)
+    ps, rows2 = _pool(scales, S, H, d // desc.group, "scales", F16)
+    if rows2 != rows:
+        raise ValueError("codes and scales must have the same rows")
+    st = lib.srftq_dequantize_paged(ctypes.byref(desc), S, N, pc, ps, rows,
+                                    _ints(slots, torch.int64, (N,), "slots"),
+                                    _table(signs, S, H, d, "signs", I8),
+                                    _table(lam, S, H, d, "lambda", F32), px, xs,
+                                    _stream_handle(stream))
+    _check("srftq_dequantize_paged", st)
+
+
+def srftq_prefix_attention_workspace(desc: SrftqDesc, n_seq: int, q_per_kv: int,
+                                     prefix_len: int) -> int:
+    """Bytes of workspace that srftq_prefix_attention needs for these sizes."""
+    n = load_library().srftq_prefix_attention_workspace(ctypes.byref(desc), int(n_seq),
+                                                        int(q_per_kv), int(prefix_len))
+    if n < 0:
+        _check("srftq_prefix_attention_workspace", n)
+    return n
+
+
+def srftq_prefix_attention(desc: SrftqDesc, q, k_codes, k_scales, k_signs, k_lambda, v_codes,
+                           v_scales, v_signs, v_lambda, page_size: int, prefix_table,
+                           prefix_len: int, block_table, seq_lens, scale: float, out, lse,
+                           workspace, stream=None) -> None:
+    """out [n_seq, H*q_per_kv, d] = softmax(scale q . khat) vhat over the pages of
+    each sequence, the first prefix_len tokens shared (see include/srftq.h).
+    Pools are [rows, H, ...] tensors; prefix_table may be None for prefix_len 0,
+    lse None; workspace is a contiguous uint8 tensor."""
+    import torch
+
+    lib = load_library()
+    F16, U8, I8, F32 = _dtypes()
+    H, d = desc.heads, desc.d
+    if not isinstance(q, torch.Tensor) or q.dtype not in (F16, torch.bfloat16):
+        raise ValueError("q: expected a float16 or bfloat16 tensor")
+    _check_tensor(q, q.dtype, "q")
+    if q.dim() != 3 or q.shape[1] % H or q.shape[2] != d or not q.is_contiguous():
+        raise ValueError(f"q: expected contiguous [n_seq, {H}*q_per_kv, {d}], got "
+                         f"{tuple(q.shape)}")
+    n_seq, q_per_kv = q.shape[0], q.shape[1] // H
+    _check_tensor(out, q.dtype, "out")
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like q")
+    cb, ng = d * desc.bits // 8, d // desc.group
+    pk, rk = _cache_rows(k_codes, H, cb, "k_codes", U8)
+    pks, rks = _cache_rows(k_scales, H, ng, "k_scales", F16)
+    pv, rv = _cache_rows(v_codes, H, cb, "v_codes", U8)
+    pvs, rvs = _cache_rows(v_scales, H, ng, "v_scales", F16)
+    if not rk == rks == rv == rvs:
+        raise ValueError("the pools must have the same rows")
+    page_size, prefix_len = int(page_size), int(prefix_len)
+    if page_size < 1 or rk % page_size:
+        raise ValueError(f"the pools' {rk} rows are no whole pages of {page_size}")
+    pt, n_pt = (0, 0) if prefix_table is None else _vector(prefix_table, torch.int32,
+                                                           "prefix_table")
+    if n_pt * page_size < prefix_len:
+        raise ValueError(f"prefix_table: {n_pt} pages do not hold {prefix_len} tokens")
+    _check_tensor(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != n_seq or not block_table.is_contiguous():
+        raise ValueError(f"block_table: expected contiguous [{n_seq}, max_pages], got "
+                         f"{tuple(block_table.shape)}")
+    if lse is not None:
+        _check_tensor(lse, F32, "lse")
+        if lse.shape != q.shape[:2] or not lse.is_contiguous():
+            raise ValueError(f"lse: expected contiguous {list(q.shape[:2])}")
+    pw, n_ws = _vector(workspace, U8, "workspace")
+    st = lib.srftq_prefix_attention(
+        ctypes.byref(desc), 0 if q.dtype == F16 else 1, n_seq, q_per_kv, q.data_ptr(), pk, pks,
+        _ints(k_signs, I8, (H, d), "k_signs"), _ints(k_lambda, F32, (H, d), "k_lambda"), pv, pvs,
+        _ints(v_signs, I8, (H, d), "v_signs"), _ints(v_lambda, F32, (H, d), "v_lambda"),
+        rk // page_size, page_size, pt, prefix_len, block_table.data_ptr(), block_table.shape[1],
+        _ints(seq_lens, torch.int32, (n_seq,), "seq_lens"), float(scale), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), pw, n_ws, _stream_handle(stream))
+    _check("srftq_prefix_attention", st)
+
+
 def srftq_probe_wait_timeout(polls: int, stream=None) -> int:
     """Launches the device-side timeout probe (see include/srftq.h); returns the status."""
     return int(load_library().srftq_probe_wait_timeout(int(polls), _stream_handle(stream)))
@@ -598,3 +769,88 @@ def dequantize_dense(codes, scales, operand, lam, d: int, group: int = 16, bits:
     xhat = torch.empty((S, N, H, d), dtype=torch.float16, device=codes.device)
     srftq_dequantize_dense(desc, codes, scales, operand, lam, xhat, stream)
     return xhat
+
+
+def _on(stream):
+    """Context in which torch allocates for work on `stream`: memory that the
+    call's end gives back is then reused in that stream's order."""
+    import torch
+
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def block_tables(cached_lens, new_lens, free_pages, block_table, page_size: int, n_slots: int,
+                 stream=None):
+    """Extends block_table in place by the pages that the new tokens need and
+    returns (slots [n_slots] int64, seq_lens [n_seq], row_start [n_seq + 1],
+    counts [3]: pages taken, pages wanted, new tokens), the last three int32.
+    n_slots is the batch's number of rows: those behind the last sequence's
+    have slot -1."""
+    import torch
+
+    n_seq, dev = cached_lens.shape[0], cached_lens.device
+    with _on(stream):
+        slots = torch.empty(n_slots, dtype=torch.int64, device=dev)
+        seq_lens = torch.empty(n_seq, dtype=torch.int32, device=dev)
+        row_start = torch.empty(n_seq + 1, dtype=torch.int32, device=dev)
+        counts = torch.empty(3, dtype=torch.int32, device=dev)
+    srftq_block_tables(cached_lens, new_lens, free_pages, block_table, page_size, slots, seq_lens,
+                       row_start, counts, stream)
+    return slots, seq_lens, row_start, counts
+
+
+def quantize_paged(x, signs, lam, slots, codes, scales, group: int = 16, bits: int = 4,
+                   rotation: int = SRFT, stream=None) -> None:
+    """Quantises x [S,N,H,d] fp16 into rows slots[r] of the pools codes
+    [S,rows,H,d*bits/8] and scales [S,rows,H,d/group] (nowhere for a negative
+    slot)."""
+    desc = make_desc(x.shape[3], x.shape[2], group, bits, rotation)
+    srftq_quantize_paged(desc, x, signs, lam, slots, codes, scales, stream)
+
+
+def dequantize_paged(codes, scales, slots, signs, lam, d: int, group: int = 16, bits: int = 4,
+                     rotation: int = SRFT, out=None, stream=None):
+    """Returns the rows slots[r] of the pools as fp16 [S,N,H,d]. Rows with a
+    negative slot are left as they were in `out`, zero without one."""
+    import torch
+
+    S, _, H, _ = codes.shape
+    if out is None:
+        with _on(stream):
+            out = torch.zeros((S, slots.shape[0], H, d), dtype=torch.float16, device=codes.device)
+    desc = make_desc(d, H, group, bits, rotation)
+    srftq_dequantize_paged(desc, codes, scales, slots, signs, lam, out, stream)
+    return out
+
+
+def prefix_attention(q, k_codes, k_scales, k_signs, k_lambda, v_codes, v_scales, v_signs,
+                     v_lambda, block_table, seq_lens, prefix_table=None, prefix_len: int = 0,
+                     page_size: int = 64, group: int = 16, bits: int = 4, rotation: int = SRFT,
+                     scale: float = None, out=None, return_lse: bool = False, workspace=None,
+                     stream=None):
+    """Decode attention over a paged cache for a batch that shares its first
+    prefix_len tokens (see srftq_prefix_attention). Returns out [n_seq,
+    H*q_per_kv, d] in q's type, or (out, lse) with the float32 log-sum-exp of
+    the scores. Without a workspace it allocates one for the call."""
+    import math
+
+    import torch
+
+    n_seq, HQ, d = q.shape
+    H = k_codes.shape[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    desc = make_desc(d, H, group, bits, rotation)
+    lse = None
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if return_lse:
+            lse = torch.empty((n_seq, HQ), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = srftq_prefix_attention_workspace(desc, n_seq, HQ // H, prefix_len)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    srftq_prefix_attention(desc, q, k_codes, k_scales, k_signs, k_lambda, v_codes, v_scales,
+                           v_signs, v_lambda, page_size, prefix_table, prefix_len, block_table,
+                           seq_lens, scale, out, lse, workspace, stream)
+    return (out, lse) if return_lse else out

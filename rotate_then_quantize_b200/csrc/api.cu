@@ -96,6 +96,32 @@ int check_dense_shape(const srftq_desc* d, bool codec) {
   return SRFTQ_OK;
 }
 
+// The paged calls: positions below 2^31 with room for a tile past the end.
+constexpr int64_t kMaxPageSize = 65536;
+constexpr int64_t kMaxPosition = (int64_t(1) << 31) - 65536;
+
+bool aligned_to(const void* p, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+int check_paged_desc(const srftq_desc* d) {
+  const int rc = check_desc(d);
+  if (rc != SRFTQ_OK) return rc;
+  return (d->d == 64 || d->d == 128 || d->d == 256) && d->group >= 16 ? SRFTQ_OK
+                                                                      : SRFTQ_ERR_UNSUPPORTED;
+}
+
+int check_prefix_sizes(const srftq_desc* desc, int64_t n_seq, int32_t q_per_kv,
+                       int64_t prefix_len) {
+  const int rc = check_paged_desc(desc);
+  if (rc != SRFTQ_OK) return rc;
+  if (n_seq < 0 || prefix_len < 0 || q_per_kv < 1) return SRFTQ_ERR_INVALID_ARG;
+  if (q_per_kv > 16 || prefix_len >= kMaxPosition || n_seq >= kMaxPosition / 16 ||
+      desc->heads >= (1 << 20))
+    return SRFTQ_ERR_UNSUPPORTED;
+  return SRFTQ_OK;
+}
+
 // Byte range [lo, hi) touched by rows 0..n_rows-1 of S slices with a stride
 // of `stride` rows of `row_bytes` each.
 struct Range {
@@ -115,6 +141,16 @@ int by_d(int d, Fn&& fn) {
   switch (d) {
     case 16: return fn(Int<16>{});
     case 32: return fn(Int<32>{});
+    case 64: return fn(Int<64>{});
+    case 128: return fn(Int<128>{});
+    case 256: return fn(Int<256>{});
+    default: return SRFTQ_ERR_UNSUPPORTED;
+  }
+}
+
+template <typename Fn>
+int by_paged_d(int d, Fn&& fn) {
+  switch (d) {
     case 64: return fn(Int<64>{});
     case 128: return fn(Int<128>{});
     case 256: return fn(Int<256>{});
@@ -501,6 +537,172 @@ int srftq_dequantize_dense(const srftq_desc* desc, int64_t n_slices, int64_t n_r
               in_slice_stride_rows, out_slice_stride_rows, nullptr, codes, scales, nullptr,
               nullptr, xhat, operand, lambda, static_cast<cudaStream_t>(stream)};
   return launch_dequantize_dense(c);
+}
+
+// ---------------------------------------------------------------------------
+// Paged cache
+// ---------------------------------------------------------------------------
+
+int srftq_block_tables(int64_t n_seq, const int32_t* cached_lens, const int32_t* new_lens,
+                       int64_t page_size, const int32_t* free_pages, int64_t n_free,
+                       int32_t* block_table, int64_t max_pages, int64_t* slots, int64_t n_slots,
+                       int32_t* seq_lens, int32_t* row_start, int32_t* counts, void* stream) {
+  if (n_seq < 0 || n_free < 0 || max_pages < 0 || n_slots < 0) return SRFTQ_ERR_INVALID_ARG;
+  if (page_size < 1 || page_size > kMaxPageSize) return SRFTQ_ERR_UNSUPPORTED;
+  if (n_seq >= kMaxPosition || n_free >= kMaxPosition || max_pages >= kMaxPosition ||
+      n_slots >= kMaxPosition)
+    return SRFTQ_ERR_UNSUPPORTED;
+  if (!row_start || !counts || (n_free > 0 && !free_pages) || (n_slots > 0 && !slots))
+    return SRFTQ_ERR_INVALID_ARG;
+  if (n_seq > 0 && (!cached_lens || !new_lens || !seq_lens || (max_pages > 0 && !block_table)))
+    return SRFTQ_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(cached_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(free_pages),
+                        static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(row_start), static_cast<const void*>(counts)})
+    if (!aligned_to(p, 4)) return SRFTQ_ERR_MISALIGNED;
+  if (!aligned_to(slots, 8)) return SRFTQ_ERR_MISALIGNED;
+  const Range outs[] = {extent(block_table, 1, 0, n_seq * max_pages, 4),
+                        extent(slots, 1, 0, n_slots, 8), extent(seq_lens, 1, 0, n_seq, 4),
+                        extent(row_start, 1, 0, n_seq + 1, 4), extent(counts, 1, 0, 3, 4)};
+  for (const Range& o : outs) {
+    for (Range in : {extent(cached_lens, 1, 0, n_seq, 4), extent(new_lens, 1, 0, n_seq, 4),
+                     extent(free_pages, 1, 0, n_free, 4)})
+      if (overlap(o, in)) return SRFTQ_ERR_INVALID_ARG;
+    for (const Range& p : outs)
+      if (&p != &o && overlap(o, p)) return SRFTQ_ERR_INVALID_ARG;
+  }
+  BlockTablesCall c{n_seq,       cached_lens, new_lens, page_size, free_pages,
+                    n_free,      block_table, max_pages, slots,    n_slots,
+                    seq_lens,    row_start,   counts,    static_cast<cudaStream_t>(stream)};
+  return launch_block_tables(c);
+}
+
+int srftq_quantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_rows,
+                         const uint16_t* x, int64_t x_slice_stride_rows, const int8_t* signs,
+                         const float* lambda, const int64_t* slots, uint8_t* codes,
+                         uint16_t* scales, int64_t pool_rows, void* stream) {
+  const int rc = check_paged_desc(desc);
+  if (rc != SRFTQ_OK) return rc;
+  if (n_slices < 0 || n_rows < 0 || pool_rows < 0) return SRFTQ_ERR_INVALID_ARG;
+  if (n_slices == 0 || n_rows == 0 || pool_rows == 0) return SRFTQ_OK;
+  if (n_rows >= kMaxPosition || n_slices >= kMaxPosition) return SRFTQ_ERR_UNSUPPORTED;
+  if (x_slice_stride_rows < n_rows) return SRFTQ_ERR_INVALID_ARG;
+  if (!x || !signs || !lambda || !slots || !codes || !scales) return SRFTQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(signs) || !aligned16(lambda) || !aligned_to(slots, 8) ||
+      !aligned16(codes) || !aligned16(scales))
+    return SRFTQ_ERR_MISALIGNED;
+  const int64_t d = desc->d, H = desc->heads;
+  const Range rc_ = extent(codes, 1, 0, n_slices * pool_rows, H * d * desc->bits / 8);
+  const Range rs = extent(scales, 1, 0, n_slices * pool_rows, H * (d / desc->group) * 2);
+  for (Range out : {rc_, rs})
+    for (Range in : {extent(x, n_slices, x_slice_stride_rows, n_rows, H * d * 2),
+                     extent(signs, n_slices, H, H, d), extent(lambda, n_slices, H, H, d * 4),
+                     extent(slots, 1, 0, n_rows, 8)})
+      if (overlap(out, in)) return SRFTQ_ERR_INVALID_ARG;
+  if (overlap(rc_, rs)) return SRFTQ_ERR_INVALID_ARG;
+  PagedCall c{desc->heads, desc->group, desc->bits, desc->rotation, n_slices, n_rows, x, nullptr,
+              x_slice_stride_rows, signs, lambda, slots, codes, scales, pool_rows,
+              static_cast<cudaStream_t>(stream)};
+  return by_paged_d(desc->d,
+                    [&](auto d_) { return launch_quantize_paged<decltype(d_)::value>(c); });
+}
+
+int srftq_dequantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_rows,
+                           const uint8_t* codes, const uint16_t* scales, int64_t pool_rows,
+                           const int64_t* slots, const int8_t* signs, const float* lambda,
+                           uint16_t* xhat, int64_t out_slice_stride_rows, void* stream) {
+  const int rc = check_paged_desc(desc);
+  if (rc != SRFTQ_OK) return rc;
+  if (n_slices < 0 || n_rows < 0 || pool_rows < 0) return SRFTQ_ERR_INVALID_ARG;
+  if (n_slices == 0 || n_rows == 0 || pool_rows == 0) return SRFTQ_OK;
+  if (n_rows >= kMaxPosition || n_slices >= kMaxPosition) return SRFTQ_ERR_UNSUPPORTED;
+  if (out_slice_stride_rows < n_rows) return SRFTQ_ERR_INVALID_ARG;
+  if (!codes || !scales || !slots || !signs || !lambda || !xhat) return SRFTQ_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned_to(slots, 8) || !aligned16(signs) ||
+      !aligned16(lambda) || !aligned16(xhat))
+    return SRFTQ_ERR_MISALIGNED;
+  const int64_t d = desc->d, H = desc->heads;
+  const Range rx = extent(xhat, n_slices, out_slice_stride_rows, n_rows, H * d * 2);
+  for (Range in : {extent(codes, 1, 0, n_slices * pool_rows, H * d * desc->bits / 8),
+                   extent(scales, 1, 0, n_slices * pool_rows, H * (d / desc->group) * 2),
+                   extent(slots, 1, 0, n_rows, 8), extent(signs, n_slices, H, H, d),
+                   extent(lambda, n_slices, H, H, d * 4)})
+    if (overlap(rx, in)) return SRFTQ_ERR_INVALID_ARG;
+  PagedCall c{desc->heads, desc->group, desc->bits, desc->rotation, n_slices, n_rows, nullptr,
+              xhat, out_slice_stride_rows, signs, lambda, slots, const_cast<uint8_t*>(codes),
+              const_cast<uint16_t*>(scales), pool_rows, static_cast<cudaStream_t>(stream)};
+  return by_paged_d(desc->d,
+                    [&](auto d_) { return launch_dequantize_paged<decltype(d_)::value>(c); });
+}
+
+int64_t srftq_prefix_attention_workspace(const srftq_desc* desc, int64_t n_seq, int32_t q_per_kv,
+                                         int64_t prefix_len) {
+  const int rc = check_prefix_sizes(desc, n_seq, q_per_kv, prefix_len);
+  if (rc != SRFTQ_OK) return rc;
+  return prefix_attention_workspace(desc->d, desc->heads, n_seq, q_per_kv, prefix_len);
+}
+
+int srftq_prefix_attention(const srftq_desc* desc, int32_t dtype, int64_t n_seq, int32_t q_per_kv,
+                           const void* q, const uint8_t* k_codes, const uint16_t* k_scales,
+                           const int8_t* k_signs, const float* k_lambda, const uint8_t* v_codes,
+                           const uint16_t* v_scales, const int8_t* v_signs,
+                           const float* v_lambda, int64_t n_pages, int64_t page_size,
+                           const int32_t* prefix_table, int64_t prefix_len,
+                           const int32_t* block_table, int64_t max_pages,
+                           const int32_t* seq_lens, float softmax_scale, void* out,
+                           float* lse_or_null, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  const int rc = check_prefix_sizes(desc, n_seq, q_per_kv, prefix_len);
+  if (rc != SRFTQ_OK) return rc;
+  if (dtype != SRFTQ_FP16 && dtype != SRFTQ_BF16) return SRFTQ_ERR_UNSUPPORTED;
+  if (n_pages < 0 || max_pages < 0) return SRFTQ_ERR_INVALID_ARG;
+  if (page_size < 1 || page_size > kMaxPageSize || n_pages >= kMaxPosition ||
+      max_pages >= kMaxPosition || max_pages * page_size >= kMaxPosition)
+    return SRFTQ_ERR_UNSUPPORTED;
+  if (!(softmax_scale - softmax_scale == 0.0f)) return SRFTQ_ERR_INVALID_ARG;   // not finite
+  if (n_seq == 0) return SRFTQ_OK;
+  if (!q || !k_codes || !k_scales || !k_signs || !k_lambda || !v_codes || !v_scales ||
+      !v_signs || !v_lambda || !seq_lens || !out || !workspace ||
+      (prefix_len > 0 && !prefix_table) || (max_pages > 0 && !block_table))
+    return SRFTQ_ERR_INVALID_ARG;
+  for (const void* p : {q, static_cast<const void*>(k_codes), static_cast<const void*>(k_scales),
+                        static_cast<const void*>(k_signs), static_cast<const void*>(k_lambda),
+                        static_cast<const void*>(v_codes), static_cast<const void*>(v_scales),
+                        static_cast<const void*>(v_signs), static_cast<const void*>(v_lambda),
+                        static_cast<const void*>(out), static_cast<const void*>(workspace)})
+    if (!aligned16(p)) return SRFTQ_ERR_MISALIGNED;
+  for (const void* p : {static_cast<const void*>(prefix_table),
+                        static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(lse_or_null)})
+    if (!aligned_to(p, 4)) return SRFTQ_ERR_MISALIGNED;
+  const int64_t need =
+      prefix_attention_workspace(desc->d, desc->heads, n_seq, q_per_kv, prefix_len);
+  if (workspace_bytes < need) return SRFTQ_ERR_INVALID_ARG;
+  const int64_t d = desc->d, H = desc->heads, HQ = H * q_per_kv, rows = n_pages * page_size;
+  const int64_t cb = H * d * desc->bits / 8, sb = H * (d / desc->group) * 2;
+  const Range outs[] = {extent(out, 1, 0, n_seq * HQ, d * 2), extent(workspace, 1, 0, 1, need),
+                        extent(lse_or_null, 1, 0, lse_or_null ? n_seq * HQ : 0, 4)};
+  for (const Range& o : outs) {
+    for (Range in :
+         {extent(q, 1, 0, n_seq * HQ, d * 2), extent(k_codes, 1, 0, rows, cb),
+          extent(v_codes, 1, 0, rows, cb), extent(k_scales, 1, 0, rows, sb),
+          extent(v_scales, 1, 0, rows, sb), extent(k_signs, 1, 0, 1, H * d),
+          extent(v_signs, 1, 0, 1, H * d), extent(k_lambda, 1, 0, 1, H * d * 4),
+          extent(v_lambda, 1, 0, 1, H * d * 4),
+          extent(prefix_table, 1, 0, (prefix_len + page_size - 1) / page_size, 4),
+          extent(block_table, 1, 0, n_seq * max_pages, 4), extent(seq_lens, 1, 0, n_seq, 4)})
+      if (overlap(o, in)) return SRFTQ_ERR_INVALID_ARG;
+    for (const Range& p : outs)
+      if (&p != &o && overlap(o, p)) return SRFTQ_ERR_INVALID_ARG;
+  }
+  PrefixAttnCall c{desc->d,   desc->heads, desc->group, desc->bits, desc->rotation, q_per_kv,
+                   n_seq,     q,           dtype == SRFTQ_BF16, k_codes, k_scales,  k_signs,
+                   k_lambda,  v_codes,     v_scales,    v_signs,    v_lambda,       n_pages,
+                   page_size, prefix_table, prefix_len, block_table, max_pages,     seq_lens,
+                   softmax_scale, out,     lse_or_null, workspace,
+                   static_cast<cudaStream_t>(stream)};
+  return launch_prefix_attention(c);
 }
 
 int srftq_probe_wait_timeout(uint32_t polls, void* stream) {

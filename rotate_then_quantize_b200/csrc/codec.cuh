@@ -129,6 +129,7 @@ struct QuantArgs {
   uint16_t* scales;       // [S][T_out][H][d/G]
   int64_t out_slice_stride_rows;
   unsigned* guard;
+  const int64_t* slots;   // paged calls: the row of the pool for each row of x
 };
 
 struct DequantArgs {
@@ -141,7 +142,16 @@ struct DequantArgs {
   uint16_t* xhat;         // [S][T_out][H][d]
   int64_t out_slice_stride_rows;
   unsigned* guard;
+  const int64_t* slots;   // paged calls: the row of the pool for each row of xhat
 };
+
+// Paged calls: the pool row of batch row `row`, -1 when the row has none
+// (past the batch, a negative slot, or a slot outside the pool's `rows`).
+__device__ __forceinline__ int64_t slot_of(const int64_t* slots, int row, int n_rows,
+                                           int64_t rows) {
+  const int64_t s = row < n_rows ? __ldg(slots + row) : -1;
+  return s < rows ? s : -1;
+}
 
 
 // Static shape of one codec configuration.
@@ -489,7 +499,11 @@ __device__ __forceinline__ void quantize_codes(const float2 (&v)[D / 2],
   }
 }
 
-template <int D, int BITS, int G, int ROT, int WPC, int NST, int MINB>
+// PAGED: row r of x goes to row slots[r] of the pool (nowhere when that is
+// negative). The input side is the same; the codes leave the staging tile as
+// 16-byte stores of whole warps, 32 vectors' chunks in order, so the HPT heads
+// of a row (contiguous in the pool) still go out as full lines.
+template <int D, int BITS, int G, int ROT, int WPC, int NST, int MINB, bool PAGED = false>
 __global__ void __launch_bounds__(WPC * 32, MINB)
     quantize_kernel(const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ CUtensorMap tm_codes, const QuantArgs a) {
@@ -517,7 +531,7 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
 
   if (lane == 0) {
     prefetch_tensormap(&tm_x);
-    if constexpr (S::CODES_TMA) prefetch_tensormap(&tm_codes);
+    if constexpr (S::CODES_TMA && !PAGED) prefetch_tensormap(&tm_codes);
     for (int s = 0; s < NST; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
@@ -634,9 +648,12 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     quantize_codes<D, BITS, G>(v, sw, words);
 
     const int row = cur.rb * rpt + rl;
-    const size_t vec = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows + row) * a.g.heads +
+    int64_t slot = row;
+    if constexpr (PAGED) slot = slot_of(a.slots, row, a.g.n_rows, a.out_slice_stride_rows);
+    const size_t vec = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
+                        (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) * a.g.heads +
                        cur.hb * hpt + hl;
-    const bool valid =
+    const bool valid = PAGED ? slot >= 0 :
         row < a.g.n_rows &&
         dbg_ok(int64_t(vec) < vec_limit(a.g.n_slices, a.out_slice_stride_rows, a.g.n_rows,
                                         a.g.heads),
@@ -656,9 +673,26 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
         sts128(swz_chunk<S::C_SPAN>(crow, cc) + piece * (S::TR * S::C_SPAN),
                make_uint4(words[4 * ci], words[4 * ci + 1], words[4 * ci + 2], words[4 * ci + 3]));
       });
-      fence_proxy_async_smem();
-      pending = true;
-      prev = cur;
+      if constexpr (PAGED) {
+        __syncwarp();
+        // chunk i of the tile: piece i % CPV of the vector of lane i / CPV
+        constexpr int CPV = S::CB / 16;
+#pragma unroll
+        for (int k = 0; k < CPV; ++k) {
+          const int i = lane + 32 * k, src = i / CPV, ci = i % CPV;
+          const int64_t to = __shfl_sync(0xffffffffu, slot, src);
+          const int piece = (ci * 16) / S::C_SPAN, cc = ((ci * 16) % S::C_SPAN) / 16;
+          const uint4 w = lds128(swz_chunk<S::C_SPAN>(swz_row<S::C_SPAN>(smem_addr(ob), src), cc) +
+                                 piece * (S::TR * S::C_SPAN));
+          const size_t v_to = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
+                               (to < 0 ? 0 : to)) * a.g.heads + cur.hb * hpt + (src & (hpt - 1));
+          if (to >= 0) reinterpret_cast<uint4*>(a.codes + v_to * S::CB)[ci] = w;
+        }
+      } else {
+        fence_proxy_async_smem();
+        pending = true;
+        prev = cur;
+      }
     } else {
       static_assert(S::CODES_TMA || S::CB == 8, "direct code path covers d=16 int4 only");
       if (valid) *reinterpret_cast<uint2*>(a.codes + vec * S::CB) = make_uint2(words[0], words[1]);
@@ -719,7 +753,12 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t sgw, float c_ev
   }
 }
 
-template <int D, int BITS, int G, int ROT, int WPC, int NST, int MINB>
+// PAGED: row r of xhat comes from row slots[r] of the pool; a row whose slot
+// is negative is left as it was. The codes are gathered with 16-byte cp.async
+// copies of whole warps into the same swizzled stage, one tile ahead, their
+// slots loaded a tile before that. A tile with such rows stores its other
+// rows from the staging tile with plain stores, any other tile with TMA.
+template <int D, int BITS, int G, int ROT, int WPC, int NST, int MINB, bool PAGED = false>
 __global__ void __launch_bounds__(WPC * 32, MINB)
     dequantize_kernel(const __grid_constant__ CUtensorMap tm_codes,
                       const __grid_constant__ CUtensorMap tm_xhat, const DequantArgs a) {
@@ -746,13 +785,36 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
   const uint32_t* mkrow = mtab + hl * Lay::kSignStride;
 
   if (lane == 0) {
-    if constexpr (S::CODES_TMA) prefetch_tensormap(&tm_codes);
+    if constexpr (S::CODES_TMA && !PAGED) prefetch_tensormap(&tm_codes);
     prefetch_tensormap(&tm_xhat);
     for (int s = 0; s < NST; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
   __syncwarp();
 
+  auto tile_slot = [&](const TileWalk& c) {
+    return c.valid() ? slot_of(a.slots, c.rb * rpt + rl, a.g.n_rows, a.in_slice_stride_rows) : -1;
+  };
+  // paged: the codes of tile c, lane l's vector being in row `slot` of its slice
+  auto gather = [&](const TileWalk& c, int64_t slot) {
+    constexpr int CPV = S::CB / 16;
+#pragma unroll
+    for (int k = 0; k < CPV; ++k) {
+      const int i = lane + 32 * k, src = i / CPV, ci = i % CPV;
+      const int64_t from = __shfl_sync(0xffffffffu, slot, src);
+      const int piece = (ci * 16) / S::C_SPAN, cc = ((ci * 16) % S::C_SPAN) / 16;
+      if (from >= 0) {
+        const size_t v = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + from) * a.g.heads +
+                         c.hb * hpt + (src & (hpt - 1));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         swz_chunk<S::C_SPAN>(swz_row<S::C_SPAN>(smem_addr(ws), src), cc) +
+                         piece * (S::TR * S::C_SPAN)),
+                     "l"(a.codes + v * S::CB + 16 * ci)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   auto issue = [&](const TileWalk& c, int st) {
     uint8_t* sb = ws + st * Lay::kInBytes;
     if (!dbg_ok(tile_in_range(c, a.g), a.guard)) {
@@ -779,9 +841,16 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     bulk_commit();
   };
 
+  static_assert(!PAGED || (NST == 1 && S::CODES_TMA), "the gather has one stage");
   TileWalk ahead = cur;
   int issued = 0;
-  if (lane == 0) {
+  int64_t slot_cur = -1, slot_next = -1;   // paged: rows of this tile and of the next
+  if constexpr (PAGED) {
+    slot_cur = tile_slot(cur);
+    gather(cur, slot_cur);
+    ahead.advance(a.g);
+    slot_next = tile_slot(ahead);
+  } else if (lane == 0) {
     for (int k = 0; k < NST && ahead.valid(); ++k) {
       issue(ahead, k);
       ++issued;
@@ -790,11 +859,12 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
   }
 
   // the next tile's scales are loaded one tile ahead, into registers
-  auto load_scales = [&](const TileWalk& c, uint32_t (&sw)[S::SW]) {
+  auto load_scales = [&](const TileWalk& c, uint32_t (&sw)[S::SW], int64_t slot) {
     const int row = c.rb * rpt + rl;
-    const size_t vec = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + row) * a.g.heads +
+    const size_t vec = (static_cast<size_t>(c.s) * a.in_slice_stride_rows +
+                        (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) * a.g.heads +
                        c.hb * hpt + hl;
-    if (row < a.g.n_rows &&
+    if (PAGED ? slot >= 0 : row < a.g.n_rows &&
         dbg_ok(int64_t(vec) < vec_limit(a.g.n_slices, a.in_slice_stride_rows, a.g.n_rows,
                                         a.g.heads),
                a.guard)) {
@@ -822,7 +892,7 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     }
   };
   uint32_t sw_next[S::SW];
-  load_scales(cur, sw_next);
+  load_scales(cur, sw_next, slot_cur);
 
   int it = 0;
   int table_key = -1;         // (slice, head block) the tables were built for
@@ -833,7 +903,7 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     const uint32_t parity = (it / NST) & 1;
     const uint8_t* sb = ws + st * Lay::kInBytes;
     const int row = cur.rb * rpt + rl;
-    const bool valid =
+    const bool valid = PAGED ? slot_cur >= 0 :
         row < a.g.n_rows &&
         dbg_ok(int64_t((static_cast<size_t>(cur.s) * a.in_slice_stride_rows + row) * a.g.heads +
                        cur.hb * hpt + hl) <
@@ -844,7 +914,7 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     static_for<0, S::SW>([&](auto k_) { sw[decltype(k_)::value] = sw_next[decltype(k_)::value]; });
     TileWalk nxt = cur;
     nxt.advance(a.g);
-    if (nxt.valid()) load_scales(nxt, sw_next);
+    if (nxt.valid()) load_scales(nxt, sw_next, slot_next);
 
     uint32_t words[S::CW];
     if constexpr (!S::CODES_TMA) {
@@ -867,7 +937,14 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
       table_key = key;
     }
 
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], parity));
+    bool landed = true;
+    if constexpr (PAGED) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+    } else {
+      landed = mbar_wait_bounded(&bars[st], parity);
+    }
+    const bool ok = PAGED || __all_sync(0xffffffffu, landed);
     if (!ok) {
       if (lane == 0) {
         atomicOr(a.guard, kGuardWaitTimeout);
@@ -896,7 +973,13 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     // the previous tile's output. Store that, and refill this stage with the
     // tile NST ahead right away.
     __syncwarp();
-    if (lane == 0) {
+    if constexpr (PAGED) {
+      if (lane == 0 && pending) store_xhat(prev);
+      if (ahead.valid()) {
+        gather(ahead, slot_next);
+        ahead.advance(a.g);
+      }
+    } else if (lane == 0) {
       if (pending) store_xhat(prev);
       if (ahead.valid()) {
         issue(ahead, st);
@@ -948,6 +1031,24 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     });
     fence_proxy_async_smem();
     pending = true;
+    if constexpr (PAGED) {
+      if (!__all_sync(0xffffffffu, valid || row >= a.g.n_rows)) {
+        pending = false;   // rows to leave alone: each lane stores its own vector
+        if (valid) {
+          uint16_t* dst = a.xhat + ((static_cast<size_t>(cur.s) * a.out_slice_stride_rows + row) *
+                                        a.g.heads + cur.hb * hpt + hl) * D;
+          static_for<0, D / 8>([&](auto c_) {
+            constexpr int ci = decltype(c_)::value;
+            constexpr int piece = (ci * 16) / S::X_SPAN;
+            constexpr int cc = ((ci * 16) % S::X_SPAN) / 16;
+            reinterpret_cast<uint4*>(dst)[ci] =
+                lds128(swz_chunk<S::X_SPAN>(xrow, cc) + piece * (S::TR * S::X_SPAN));
+          });
+        }
+      }
+      slot_cur = slot_next;
+      slot_next = tile_slot(ahead);
+    }
     prev = cur;
     cur = nxt;
   }

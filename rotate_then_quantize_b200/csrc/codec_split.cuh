@@ -413,7 +413,9 @@ __device__ __forceinline__ int split_group(int g, int role) {
 // Quantiser
 // ---------------------------------------------------------------------------
 
-template <int D, int BITS, int G, int ROT, int MINB>
+// PAGED: as in codec.cuh, row r of x goes to row slots[r] of the pool; the
+// codes leave the staging tile with plain 16-byte stores of both warps.
+template <int D, int BITS, int G, int ROT, int MINB, bool PAGED = false>
 __global__ void __launch_bounds__(64, MINB)
     quantize_split_kernel(const __grid_constant__ CUtensorMap tm_x,
                           const __grid_constant__ CUtensorMap tm_codes, const QuantArgs a) {
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(64, MINB)
 
   if (leader) {
     prefetch_tensormap(&tm_x);
-    prefetch_tensormap(&tm_codes);
+    if constexpr (!PAGED) prefetch_tensormap(&tm_codes);
     mbar_init(bar, 1);
     fence_barrier_init();
   }
@@ -633,15 +635,32 @@ __global__ void __launch_bounds__(64, MINB)
       sts128(code_chunk_addr<S>(crow, cg),
              make_uint4(words[4 * k], words[4 * k + 1], words[4 * k + 2], words[4 * k + 3]));
     });
-    fence_proxy_async_smem();
-    pending = true;
-    prev = cur;
+    const int row = cur.rb * rpt + rl;
+    int64_t slot = row;
+    if constexpr (PAGED) {
+      slot = slot_of(a.slots, row, a.g.n_rows, a.out_slice_stride_rows);
+      bar_pair();   // both roles' chunks are staged
+      constexpr int CPV = S::CB / 16;
+#pragma unroll
+      for (int k = 0; k < CPV / 2; ++k) {
+        const int i = tid + 64 * k, src = i / CPV, ci = i % CPV;
+        const int64_t to = __shfl_sync(0xffffffffu, slot, src);
+        const uint4 w = lds128(code_chunk_addr<S>(swz_row<S::C_SPAN>(smem_addr(ob), src), ci));
+        const size_t v_to = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
+                             (to < 0 ? 0 : to)) * a.g.heads + cur.hb * hpt + (src & (hpt - 1));
+        if (to >= 0) reinterpret_cast<uint4*>(a.codes + v_to * S::CB)[ci] = w;
+      }
+    } else {
+      fence_proxy_async_smem();
+      pending = true;
+      prev = cur;
+    }
 
     // (f) this role's scales; consecutive global groups go out as words
-    const int row = cur.rb * rpt + rl;
-    const size_t svec = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows + row) *
+    const size_t svec = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
+                         (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) *
                             a.g.heads + cur.hb * hpt + hl;
-    if (row < a.g.n_rows &&
+    if (PAGED ? slot >= 0 : row < a.g.n_rows &&
         dbg_ok(int64_t(svec) < vec_limit(a.g.n_slices, a.out_slice_stride_rows, a.g.n_rows,
                                          a.g.heads),
                a.guard)) {
@@ -710,7 +729,8 @@ __device__ __forceinline__ void split_dif(float2& a, float2& b) {
   }
 }
 
-template <int D, int BITS, int G, int ROT, int MINB>
+// PAGED: as in codec.cuh, row r of xhat comes from row slots[r] of the pool.
+template <int D, int BITS, int G, int ROT, int MINB, bool PAGED = false>
 __global__ void __launch_bounds__(64, MINB)
     dequantize_split_kernel(const __grid_constant__ CUtensorMap tm_codes,
                             const __grid_constant__ CUtensorMap tm_xhat, const DequantArgs a) {
@@ -747,7 +767,7 @@ __global__ void __launch_bounds__(64, MINB)
   const uint32_t partner_row = xch + (1 - role) * Lay::kXchWarp + lane * Lay::kXchLane;
 
   if (leader) {
-    prefetch_tensormap(&tm_codes);
+    if constexpr (!PAGED) prefetch_tensormap(&tm_codes);
     prefetch_tensormap(&tm_xhat);
     mbar_init(bar, 1);
     fence_barrier_init();
@@ -774,9 +794,36 @@ __global__ void __launch_bounds__(64, MINB)
     }
     bulk_commit();
   };
+  auto tile_slot = [&](const TileWalk& c) {
+    return c.valid() ? slot_of(a.slots, c.rb * rpt + rl, a.g.n_rows, a.in_slice_stride_rows) : -1;
+  };
+  // paged: the codes of tile c, lane l's vector being in row `slot` of its slice
+  auto gather = [&](const TileWalk& c, int64_t slot) {
+    constexpr int CPV = S::CB / 16;
+#pragma unroll
+    for (int k = 0; k < CPV / 2; ++k) {
+      const int i = tid + 64 * k, src = i / CPV, ci = i % CPV;
+      const int64_t from = __shfl_sync(0xffffffffu, slot, src);
+      if (from >= 0) {
+        const size_t v = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + from) * a.g.heads +
+                         c.hb * hpt + (src & (hpt - 1));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         code_chunk_addr<S>(swz_row<S::C_SPAN>(smem_addr(sb), src), ci)),
+                     "l"(a.codes + v * S::CB + 16 * ci)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 
   TileWalk ahead = cur;
-  if (leader) {
+  int64_t slot_cur = -1, slot_next = -1;   // paged: rows of this tile and of the next
+  if constexpr (PAGED) {
+    slot_cur = tile_slot(cur);
+    gather(cur, slot_cur);
+    ahead.advance(a.g);
+    slot_next = tile_slot(ahead);
+  } else if (leader) {
     issue(ahead);
     ahead.advance(a.g);
   }
@@ -789,11 +836,12 @@ __global__ void __launch_bounds__(64, MINB)
   constexpr int NSW = Grp::kLocal ? S::NGR / 2 : 1;
   constexpr int LGS = Grp::kLocal ? S::GS : Grp::LGS;
   constexpr bool kWords = ROT == kSRHT || S::kScaleWords;
-  auto load_scales = [&](const TileWalk& c, uint32_t (&rs)[NSW], uint32_t& ex) {
+  auto load_scales = [&](const TileWalk& c, uint32_t (&rs)[NSW], uint32_t& ex, int64_t slot) {
     const int row = c.rb * rpt + rl;
-    const size_t svec = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + row) * a.g.heads +
+    const size_t svec = (static_cast<size_t>(c.s) * a.in_slice_stride_rows +
+                         (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) * a.g.heads +
                         c.hb * hpt + hl;
-    if (row < a.g.n_rows &&
+    if (PAGED ? slot >= 0 : row < a.g.n_rows &&
         dbg_ok(int64_t(svec) < vec_limit(a.g.n_slices, a.in_slice_stride_rows, a.g.n_rows,
                                          a.g.heads),
                a.guard)) {
@@ -823,7 +871,7 @@ __global__ void __launch_bounds__(64, MINB)
     }
   };
   uint32_t rs_next[NSW], ex_next = 0u;
-  load_scales(cur, rs_next, ex_next);
+  load_scales(cur, rs_next, ex_next, slot_cur);
 
   int it = 0;
   int table_key = -1;
@@ -835,7 +883,7 @@ __global__ void __launch_bounds__(64, MINB)
     const uint32_t ex = ex_next;
     TileWalk nxt = cur;
     nxt.advance(a.g);
-    if (nxt.valid()) load_scales(nxt, rs_next, ex_next);
+    if (nxt.valid()) load_scales(nxt, rs_next, ex_next, slot_next);
 
     const int key = cur.table_key(a.g);
     if (key != table_key) {
@@ -843,7 +891,13 @@ __global__ void __launch_bounds__(64, MINB)
           mult, mtab, a.lambda, a.signs, cur.s, cur.hb, a.g.heads, hpt_log2, tid);
       table_key = key;
     }
-    const bool ok = __syncthreads_and(mbar_wait_bounded(bar, it & 1)) != 0;
+    bool ok = true;
+    if constexpr (PAGED) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+    } else {
+      ok = __syncthreads_and(mbar_wait_bounded(bar, it & 1)) != 0;
+    }
     if (!ok) {
       if (leader) {
         atomicOr(a.guard, kGuardWaitTimeout);
@@ -883,7 +937,13 @@ __global__ void __launch_bounds__(64, MINB)
     // Both warps have read the stage and staged + fenced the previous
     // tile's output: store it and refill the stage with the next tile.
     bar_pair();
-    if (leader) {
+    if constexpr (PAGED) {
+      if (leader && pending) store_xhat(prev);
+      if (ahead.valid()) {
+        gather(ahead, slot_next);
+        ahead.advance(a.g);
+      }
+    } else if (leader) {
       if (pending) store_xhat(prev);
       if (ahead.valid()) {
         issue(ahead);
@@ -1051,6 +1111,23 @@ __global__ void __launch_bounds__(64, MINB)
     }
     fence_proxy_async_smem();
     pending = true;
+    if constexpr (PAGED) {
+      const int row = cur.rb * rpt + rl;
+      // both warps hold the same rows, so they agree
+      if (!__all_sync(0xffffffffu, slot_cur >= 0 || row >= a.g.n_rows)) {
+        pending = false;   // rows to leave alone: each warp stores half of its lanes' vectors
+        bar_pair();
+        if (slot_cur >= 0) {
+          uint16_t* dst = a.xhat + ((static_cast<size_t>(cur.s) * a.out_slice_stride_rows + row) *
+                                        a.g.heads + cur.hb * hpt + hl) * D;
+#pragma unroll 4
+          for (int ci = role * (S::XC / 2); ci < (role + 1) * (S::XC / 2); ++ci)
+            reinterpret_cast<uint4*>(dst)[ci] = lds128(row_chunk(xrow, ci));
+        }
+      }
+      slot_cur = slot_next;
+      slot_next = tile_slot(ahead);
+    }
     prev = cur;
     cur = nxt;
   }

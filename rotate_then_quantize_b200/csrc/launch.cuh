@@ -146,6 +146,72 @@ int launch_quantize_dense(const DenseCall& c);
 int launch_dequantize_dense(const DenseCall& c);
 int launch_calibrate_dense(const DenseCalibCall& c);
 
+// Paged cache (launch_block_tables.cu, launch_paged_d*.cu, launch_paged_attention.cu).
+struct BlockTablesCall {
+  int64_t n_seq;
+  const int32_t* cached_lens;
+  const int32_t* new_lens;
+  int64_t page_size;
+  const int32_t* free_pages;
+  int64_t n_free;
+  int32_t* block_table;
+  int64_t max_pages;
+  int64_t* slots;
+  int64_t n_slots;
+  int32_t* seq_lens;
+  int32_t* row_start;
+  int32_t* counts;
+  cudaStream_t stream;
+};
+
+struct PagedCall {
+  int32_t heads, group, bits, rotation;
+  int64_t n_slices, n_rows;
+  const uint16_t* x;       // quantise: the rows
+  uint16_t* xhat;          // dequantise: the rows
+  int64_t x_stride_rows;
+  const int8_t* signs;
+  const float* lambda;
+  const int64_t* slots;
+  uint8_t* codes;
+  uint16_t* scales;
+  int64_t pool_rows;       // rows of a slice of the pool, and its slice stride
+  cudaStream_t stream;
+};
+
+struct PrefixAttnCall {
+  int32_t d, heads, group, bits, rotation, q_per_kv;
+  int64_t n_seq;
+  const void* q;
+  bool bf16;
+  const uint8_t* k_codes;
+  const uint16_t* k_scales;
+  const int8_t* k_signs;
+  const float* k_lambda;
+  const uint8_t* v_codes;
+  const uint16_t* v_scales;
+  const int8_t* v_signs;
+  const float* v_lambda;
+  int64_t n_pages, page_size;
+  const int32_t* prefix_table;
+  int64_t prefix_len;
+  const int32_t* block_table;
+  int64_t max_pages;
+  const int32_t* seq_lens;
+  float scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  cudaStream_t stream;
+};
+
+int launch_block_tables(const BlockTablesCall& c);
+template <int D> int launch_quantize_paged(const PagedCall& c);
+template <int D> int launch_dequantize_paged(const PagedCall& c);
+int64_t prefix_attention_workspace(int32_t d, int32_t heads, int64_t n_seq, int32_t q_per_kv,
+                                   int64_t prefix_len);
+int launch_prefix_attention(const PrefixAttnCall& c);
+
 // Services the per-d units get from the API unit.
 struct Runtime {
   // Encodes a rank-4 tiled tensor map; returns 0 on success.

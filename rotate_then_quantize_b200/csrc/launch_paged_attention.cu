@@ -1,0 +1,116 @@
+// Launcher of the shared-prefix attention over a paged cache (paged_attention.cuh).
+#include <climits>
+
+#include "launch_impl.cuh"
+#include "paged_attention.cuh"
+
+namespace srftq {
+namespace {
+
+// Sizes of a call that the caller's workspace and the launches follow from:
+// host values only, none of them dependent on the sequences' lengths.
+struct PrefixShape {
+  int32_t splits, per, chunk_goal;
+  int64_t q_off, plan_off, start_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
+};
+
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int64_t prefix_len,
+                         int sms) {
+  PrefixShape s{};
+  const int64_t rows = n_seq * g;
+  const int64_t tiles = (rows + kPrefixRows - 1) / kPrefixRows * heads;
+  if (prefix_len > 0) {
+    // parts enough for four blocks per SM, of at least 64 tokens
+    int64_t n = (4 * int64_t(sms) + tiles - 1) / tiles;
+    const int64_t most = (prefix_len + 63) / 64;
+    n = n < 1 ? 1 : n > most ? most : n;
+    const int64_t per = ((prefix_len + n - 1) / n + 63) / 64 * 64;
+    s.per = int32_t(per);
+    s.splits = int32_t((prefix_len + per - 1) / per);
+  }
+  s.chunk_goal = int32_t((8 * int64_t(sms) + heads - 1) / heads);
+  const int64_t chunks = s.chunk_goal + n_seq;
+  int64_t o = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = o;
+    o += up16(bytes);
+    return at;
+  };
+  s.q_off = take(n_seq * heads * g * d * 4);
+  s.plan_off = take(sizeof(PrefixPlan));
+  s.start_off = take((n_seq + 1) * 4);
+  s.pre_ml_off = take(s.splits * heads * rows * 8);
+  s.pre_acc_off = take(s.splits * heads * rows * d * 4);
+  s.own_ml_off = take(chunks * heads * g * 8);
+  s.own_acc_off = take(chunks * heads * g * d * 4);
+  s.bytes = o;
+  return s;
+}
+
+}  // namespace
+
+int64_t prefix_attention_workspace(int32_t d, int32_t heads, int64_t n_seq, int32_t q_per_kv,
+                                   int64_t prefix_len) {
+  return prefix_shape(d, heads, n_seq, q_per_kv, prefix_len, Runtime::num_sms()).bytes;
+}
+
+int launch_prefix_attention(const PrefixAttnCall& c) {
+  const int sms = Runtime::num_sms();
+  const PrefixShape s = prefix_shape(c.d, c.heads, c.n_seq, c.q_per_kv, c.prefix_len, sms);
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  PrefixArgs a{};
+  a.n_seq = int32_t(c.n_seq);
+  a.heads = c.heads;
+  a.q_per_kv = c.q_per_kv;
+  a.lg_group = ilog2(c.group);
+  a.prefix_len = int32_t(c.prefix_len);
+  a.max_pages = int32_t(c.max_pages);
+  a.prefix_splits = s.splits;
+  a.prefix_per = s.per;
+  a.chunk_goal = s.chunk_goal;
+  a.map = PageMap{FastDiv::make(uint32_t(c.page_size)), int32_t(c.n_pages)};
+  a.q = c.q;
+  a.bf16 = c.bf16;
+  a.k_codes = c.k_codes;
+  a.k_scales = c.k_scales;
+  a.k_signs = c.k_signs;
+  a.k_lambda = c.k_lambda;
+  a.v_codes = c.v_codes;
+  a.v_scales = c.v_scales;
+  a.v_signs = c.v_signs;
+  a.v_lambda = c.v_lambda;
+  a.prefix_table = c.prefix_table;
+  a.block_table = c.block_table;
+  a.seq_lens = c.seq_lens;
+  a.scale = c.scale;
+  a.out = c.out;
+  a.lse = c.lse;
+  a.qrot = reinterpret_cast<float*>(ws + s.q_off);
+  a.plan = reinterpret_cast<PrefixPlan*>(ws + s.plan_off);
+  a.chunk_start = reinterpret_cast<int32_t*>(ws + s.start_off);
+  a.pre_ml = reinterpret_cast<float2*>(ws + s.pre_ml_off);
+  a.pre_acc = reinterpret_cast<float*>(ws + s.pre_acc_off);
+  a.own_ml = reinterpret_cast<float2*>(ws + s.own_ml_off);
+  a.own_acc = reinterpret_cast<float*>(ws + s.own_acc_off);
+  const int64_t queries = c.n_seq * c.heads * c.q_per_kv;
+  const int64_t blocks = (queries + 7) / 8;   // a warp per query
+  if (blocks > INT_MAX) return SRFTQ_ERR_UNSUPPORTED;
+  int rc = SRFTQ_ERR_UNSUPPORTED;
+  static_for<6, 9>([&](auto lg_) {
+    constexpr int D = 1 << decltype(lg_)::value;
+    if (c.d != D) return;
+    const int g1 = int(blocks < 8 * sms ? blocks : 8 * sms);
+    if (c.rotation == kSRFT) prefix_prepare_kernel<kSRFT, D><<<g1, 256, 0, c.stream>>>(a);
+    else prefix_prepare_kernel<kSRHT, D><<<g1, 256, 0, c.stream>>>(a);
+    if (c.bits == 4) prefix_partial_kernel<D, 4><<<8 * sms, kPrefixWarps * 32, 0, c.stream>>>(a);
+    else prefix_partial_kernel<D, 8><<<8 * sms, kPrefixWarps * 32, 0, c.stream>>>(a);
+    if (c.rotation == kSRFT) prefix_merge_kernel<kSRFT, D><<<int(blocks), 256, 0, c.stream>>>(a);
+    else prefix_merge_kernel<kSRHT, D><<<int(blocks), 256, 0, c.stream>>>(a);
+    rc = finish_launch();
+  });
+  return rc;
+}
+
+}  // namespace srftq
