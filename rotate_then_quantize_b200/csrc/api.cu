@@ -658,7 +658,8 @@ int srftq_prefix_attention(const srftq_desc* desc, int32_t dtype, int64_t n_seq,
   if (dtype != SRFTQ_FP16 && dtype != SRFTQ_BF16) return SRFTQ_ERR_UNSUPPORTED;
   if (n_pages < 0 || max_pages < 0) return SRFTQ_ERR_INVALID_ARG;
   if (page_size < 1 || page_size > kMaxPageSize || n_pages >= kMaxPosition ||
-      max_pages >= kMaxPosition || max_pages * page_size >= kMaxPosition)
+      n_pages * page_size >= kMaxPosition || max_pages >= kMaxPosition ||
+      max_pages * page_size >= kMaxPosition)
     return SRFTQ_ERR_UNSUPPORTED;
   if (!(softmax_scale - softmax_scale == 0.0f)) return SRFTQ_ERR_INVALID_ARG;   // not finite
   if (n_seq == 0) return SRFTQ_OK;

@@ -5,6 +5,10 @@
 #include "paged_attention.cuh"
 
 namespace srftq {
+
+template <int D>
+int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t stream);
+
 namespace {
 
 // Sizes of a call that the caller's workspace and the launches follow from:
@@ -104,8 +108,8 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
     const int g1 = int(blocks < 8 * sms ? blocks : 8 * sms);
     if (c.rotation == kSRFT) prefix_prepare_kernel<kSRFT, D><<<g1, 256, 0, c.stream>>>(a);
     else prefix_prepare_kernel<kSRHT, D><<<g1, 256, 0, c.stream>>>(a);
-    if (c.bits == 4) prefix_partial_kernel<D, 4><<<8 * sms, kPrefixWarps * 32, 0, c.stream>>>(a);
-    else prefix_partial_kernel<D, 8><<<8 * sms, kPrefixWarps * 32, 0, c.stream>>>(a);
+    rc = launch_prefix_tiles<D>(a, c.bits, c.group, c.stream);
+    if (rc != SRFTQ_OK) return;
     if (c.rotation == kSRFT) prefix_merge_kernel<kSRFT, D><<<int(blocks), 256, 0, c.stream>>>(a);
     else prefix_merge_kernel<kSRHT, D><<<int(blocks), 256, 0, c.stream>>>(a);
     rc = finish_launch();

@@ -1,0 +1,4 @@
+// Shared-prefix attention parts for head dimension d = 256.
+#include "launch_prefix_tiles.cuh"
+
+template int srftq::launch_prefix_tiles<256>(const srftq::PrefixArgs&, int, int, cudaStream_t);

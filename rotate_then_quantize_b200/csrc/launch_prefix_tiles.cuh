@@ -1,0 +1,33 @@
+// Launcher of the parts kernel of the shared-prefix attention; each head
+// dimension is compiled in its own unit (launch_prefix_d*.cu).
+#pragma once
+
+#include "launch_impl.cuh"
+#include "paged_attention.cuh"
+
+namespace srftq {
+
+template <int D>
+int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t stream) {
+  int rc = SRFTQ_ERR_UNSUPPORTED;
+  static_for<0, 2>([&](auto b_) {
+    constexpr int BITS = decltype(b_)::value == 0 ? 4 : 8;
+    static_for<4, ilog2(D) + 1>([&](auto lg_) {
+      constexpr int G = 1 << decltype(lg_)::value;
+      static_for<0, 2>([&](auto e_) {
+        constexpr bool EXACT = decltype(e_)::value != 0;
+        if (bits != BITS || group != G || EXACT == a.bf16) return;
+        constexpr auto K = prefix_tile_kernel<D, BITS, G, EXACT>;
+        constexpr int smem = TileLayout<D, BITS, G>::kBytes;
+        int bps = 0;
+        rc = prepare_kernel<K>(smem, kTileWarps * 32, &bps);
+        if (rc != SRFTQ_OK) return;
+        K<<<Runtime::num_sms() * bps, kTileWarps * 32, smem, stream>>>(a);
+        rc = finish_launch();
+      });
+    });
+  });
+  return rc;
+}
+
+}  // namespace srftq

@@ -19,7 +19,7 @@
 //   prefix_prepare_kernel   a warp per query: lambda_K * R_K (s_K q) * scale *
 //                           log2 e into the workspace; block 0 also plans the
 //                           split of the sequences' own tokens;
-//   prefix_partial_kernel   the parts, each (m, l, a) into the workspace;
+//   prefix_tile_kernel      the parts, each (m, l, a) into the workspace;
 //   prefix_merge_kernel     a warp per query head: joins its parts, applies
 //                           lambda_V / l, R_V^T and s_V, rounds once.
 #pragma once
@@ -34,7 +34,6 @@
 namespace srftq {
 
 constexpr int kPrefixRows = 8;        // query rows of one item
-constexpr int kPrefixWarps = 4;       // warps of a block, each with its own online softmax
 constexpr int kPrefixMaxG = 16;       // query heads per KV head
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -170,140 +169,552 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
   if (blockIdx.x == 0) plan_own_tokens(a);
 }
 
-// sigma * code of this lane's EP consecutive coordinates of a pool row.
-template <int D, int BITS>
-__device__ __forceinline__ void lane_values(const uint8_t* codes, float sigma, int lane,
-                                            float (&v)[D / 32]) {
-  constexpr int EP = D / 32, NB = EP * BITS / 8;
-  const int8_t* p = reinterpret_cast<const int8_t*>(codes) + lane * NB;
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int c = p[i];
-    if constexpr (BITS == 8) {
-      v[i] = sigma * float(c);
-    } else {
-      v[2 * i] = sigma * float((c << 28) >> 28);
-      v[2 * i + 1] = sigma * float(c >> 4);
-    }
-  }
+// ---------------------------------------------------------------------------
+// Parts on the warp-level tensor cores (mma.sync)
+// ---------------------------------------------------------------------------
+//
+// An item is up to 8 query rows x a range of tokens of one head. A warp takes
+// 32 tokens at a time through a ring of cp.async stages and keeps its own
+// online softmax. Tokens are the rows of both products' left operands:
+//
+// Scores, S[token][query] = sum_G sigma_G D_G, D_G = sum_{j in G} c_j q_j, one
+// m16n8k16 per 16 coordinates. The codes enter exactly: with u = c + 8 (int4)
+// or c + 128 (int8), the 16-bit pattern u is the fp16 subnormal u 2^-24, so one
+// AND-XOR makes two operands of a packed word. The offset leaves through one
+// more product, of the scales (fp16, exact) with -8 2^-24 sum_{j in G} q_j. The
+// query is scaled by a power of two to [2^13, 2^14) and held as fp16 hi (+ lo
+// when the output is fp16). The scale multiplies D_G in float32, so a score's
+// only rounding to fewer bits is the query's: 2^-12 for bf16 outputs (whose own
+// step is 2^-9), 2^-23 for fp16.
+//
+// Values, O[coord][query] += sum_t (sigma c / 128)[coord][t] p'[t][query], p' =
+// 2^15 e^{x - m} (the factor keeps small weights normal). sigma c / 128 is
+// rounded once to fp16: at most |sigma|, so it never overflows. The 8-bit
+// transposing ldmatrix gives lane (g, t) coordinate g of tokens 4t .. 4t + 3,
+// and the score rows take their tokens in the order that hands the lane's p'
+// over with one movmatrix. p' is fp16 hi (+ lo for fp16 outputs).
+//
+// What bounds it: codes and scales of a vector are read once per 8 queries;
+// about 20 instructions per token and warp against 7 clocks of its memory time
+// at d = 128, int4.
+
+constexpr int kTileWarps = 4;
+constexpr int kTileChunk = 32;   // tokens a warp takes at a time
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void ldmatrix_bytes_trans(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0, %1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// The part of (x, y) that their fp16 roundings h leave, rounded to fp16.
+__device__ __forceinline__ uint32_t half2_rest(float x, float y, uint32_t h) {
+  const float2 f = unpack_half2(h);
+  return pack_half2(x - f.x, y - f.y);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 16 bytes of global memory to shared memory, zeros where !on.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+               "r"(on ? BYTES : 0)
+               : "memory");
 }
 
-// One item: rows (query rows) x tokens [t0, t1) of one head, by a block.
-template <int D, int BITS>
-__global__ void __launch_bounds__(kPrefixWarps * 32) prefix_partial_kernel(const PrefixArgs a) {
-  constexpr int EP = D / 32, CB = D * BITS / 8, R = kPrefixRows, NW = kPrefixWarps;
-  __shared__ float acc_sh[NW][R][D];
-  __shared__ float2 ml_sh[NW][R];
+// Shared memory of one warp: kStages stages of 32 tokens. Rows are padded by 16
+// bytes, which puts the 8 rows that a load of any kind here touches together on
+// distinct banks. Scale rows are 16 bytes at least, their unused part zero.
+template <int D, int BITS, int G>
+struct TileLayout {
+  static constexpr int CB = D * BITS / 8, NG = D / G, NS16 = D / 16;
+  static constexpr int RS = CB + 16;
+  static constexpr int SB = 2 * NG, SBS = SB < 16 ? 16 : SB;
+  static constexpr int kK = 0, kV = 32 * RS, kKS = 64 * RS, kVS = kKS + 32 * SBS;
+  static constexpr int kStage = kVS + 32 * SBS;
+  static constexpr int kStages = 2;
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kMl = kTileWarps * kWarp;             // the warps' (m, l) of 8 rows
+  static constexpr int kBytes = kMl + kTileWarps * 8 * 8;
+  static_assert(kWarp >= 8 * D * 4, "a warp's partial sums fit over its stages");
+};
+
+// The item's rows and tokens (shared by the kernels below).
+struct PartItem {
+  int h, b, r0, nr, t0, t1;
+  bool pre;
+  int64_t part;
+  const int32_t* table;
+};
+
+// Own-token item i: chunk c of a sequence, head h, row tile rt.
+__device__ __forceinline__ PartItem own_item(const PrefixArgs& a, int64_t i, int tiles) {
+  PartItem p;
+  p.pre = false;
+  const int rt = int(i % tiles);
+  const int64_t q = i / tiles;
+  p.h = int(q % a.heads);
+  const int c = int(q / a.heads);
+  int lo = 0, hi = a.n_seq;   // the sequence of chunk c: last start <= c
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.chunk_start + mid) <= c) lo = mid; else hi = mid;
+  }
+  p.b = lo;
+  p.r0 = rt * kPrefixRows;
+  p.nr = min(kPrefixRows, a.q_per_kv - p.r0);
+  p.t0 = a.prefix_len + (c - a.chunk_start[lo]) * a.plan->chunk;
+  p.t1 = min(p.t0 + a.plan->chunk, a.len(lo));
+  p.part = (int64_t(c) * a.heads + p.h) * a.q_per_kv + p.r0;
+  p.table = a.block_table + int64_t(lo) * a.max_pages;
+  return p;
+}
+// Prefix item i: part s of the prefix, head h, row tile rt.
+__device__ __forceinline__ PartItem pre_item(const PrefixArgs& a, int64_t i, int tiles) {
+  PartItem p;
+  p.pre = true;
+  const int M = a.n_seq * a.q_per_kv;
+  const int rt = int(i % tiles);
+  const int64_t q = i / tiles;
+  p.h = int(q % a.heads);
+  const int s = int(q / a.heads);
+  p.b = 0;
+  p.r0 = rt * kPrefixRows;
+  p.nr = min(kPrefixRows, M - p.r0);
+  p.t0 = s * a.prefix_per;
+  p.t1 = min(p.t0 + a.prefix_per, a.prefix_len);
+  p.part = (int64_t(s) * a.heads + p.h) * M + p.r0;
+  p.table = a.prefix_table;
+  return p;
+}
+
+template <int D, int BITS, int G, bool EXACT>
+__global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
+    prefix_tile_kernel(const PrefixArgs a) {
+  using L = TileLayout<D, BITS, G>;
+  constexpr int CB = L::CB, NG = L::NG, NS = L::kStages, S16 = L::NS16, NW = kTileWarps;
+  constexpr int PPT = CB / 16;          // 16-byte pieces of a row
+  extern __shared__ __align__(128) uint8_t smem[];
+  float2(*ml_sh)[8] = reinterpret_cast<float2(*)[8]>(smem + L::kMl);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = a.q_per_kv, hq = a.heads * g;
-  const int M = a.n_seq * g;                             // query rows of a head
-  const int pre_tiles = a.prefix_len > 0 ? (M + R - 1) / R : 0;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ws = smem + warp * L::kWarp;
+  const uint32_t ws_a = smem_addr(ws);
+  const int qpk = a.q_per_kv, hq = a.heads * qpk;
+  const int M = a.n_seq * qpk;
+  const int pre_tiles = a.prefix_len > 0 ? (M + kPrefixRows - 1) / kPrefixRows : 0;
   const int64_t n_pre = int64_t(a.prefix_splits) * a.heads * pre_tiles;
-  const int own_tiles = (g + R - 1) / R;
-  const int64_t n_own = int64_t(a.plan->n_chunks) * a.heads * own_tiles;
-  const int NG = D >> a.lg_group;
-  for (int64_t it = blockIdx.x; it < n_pre + n_own; it += gridDim.x) {
-    const bool pre = it < n_pre;
-    int h, r0, nr, t0, t1, b = 0;
-    int64_t part;                // index of the part's first row
-    const int32_t* table;
-    if (pre) {
-      const int rt = int(it % pre_tiles);
-      const int64_t q = it / pre_tiles;
-      h = int(q % a.heads);
-      const int s = int(q / a.heads);
-      r0 = rt * R;
-      nr = min(R, M - r0);
-      t0 = s * a.prefix_per;
-      t1 = min(t0 + a.prefix_per, a.prefix_len);
-      part = (int64_t(s) * a.heads + h) * M + r0;
-      table = a.prefix_table;
-    } else {
-      const int64_t i = it - n_pre;
-      const int rt = int(i % own_tiles);
-      const int64_t q = i / own_tiles;
-      h = int(q % a.heads);
-      const int c = int(q / a.heads);
-      int lo = 0, hi = a.n_seq;   // the sequence of chunk c: last start <= c
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.chunk_start[mid] <= c) lo = mid; else hi = mid;
+  const int own_tiles = (qpk + kPrefixRows - 1) / kPrefixRows;
+  const int64_t n_items = n_pre + int64_t(a.plan->n_chunks) * a.heads * own_tiles;
+
+  for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
+    const PartItem p = it < n_pre ? pre_item(a, it, pre_tiles) : own_item(a, it - n_pre, own_tiles);
+    const int n_chunks = max(0, (p.t1 - p.t0 - kTileChunk * warp + kTileChunk * NW - 1) /
+                                    (kTileChunk * NW));
+    // zero the unused part of the scale rows (partial sums lay there before)
+    if constexpr (L::SB < 16) {
+      for (int st = 0; st < NS; ++st) {
+        *reinterpret_cast<uint4*>(ws + st * L::kStage + L::kKS + lane * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(ws + st * L::kStage + L::kVS + lane * 16) = make_uint4(0, 0, 0, 0);
       }
-      b = lo;
-      r0 = rt * R;
-      nr = min(R, g - r0);
-      t0 = a.prefix_len + (c - a.chunk_start[b]) * a.plan->chunk;
-      t1 = min(t0 + a.plan->chunk, a.len(b));
-      part = (int64_t(c) * a.heads + h) * g + r0;
-      table = a.block_table + int64_t(b) * a.max_pages;
+      __syncwarp();
     }
-    float q[R][EP], acc[R][EP], m[R], l[R];
-    int lim[R];                  // tokens that the row sees
+
+    // pool row of this lane's token of chunk c, -1 for none
+    auto row_of = [&](int c) {
+      const int tok = p.t0 + kTileChunk * (warp + NW * c) + lane;
+      return c < n_chunks && tok < p.t1 ? int32_t(a.map.row(p.table, uint32_t(tok))) : -1;
+    };
+    // copies chunk c, this lane's token in pool row `row`, into stage c % NS
+    auto issue = [&](int c, int32_t row) {
+      if (c < n_chunks) {
+        const uint32_t st = ws_a + uint32_t(c % NS) * L::kStage;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int rr = r0 + min(r, nr - 1);
-      const int bb = pre ? rr / g : b;
-      const int64_t v = int64_t(bb) * hq + h * g + (pre ? rr % g : rr);
-      lim[r] = a.len(bb);
+        for (int k = 0; k < PPT; ++k) {
+          const int i = lane + 32 * k, tok = i / PPT, pc = i % PPT;
+          const int32_t r = __shfl_sync(0xffffffffu, row, tok);
+          const int64_t vec = int64_t(r < 0 ? 0 : r) * a.heads + p.h;
+          // score rows: token 2i in row i, token 2i + 1 in row i + 8 of each 16
+          const int kr = (tok & 16) | ((tok & 1) << 3) | ((tok & 15) >> 1);
+          copy16(st + L::kK + kr * L::RS + pc * 16, a.k_codes + vec * CB + pc * 16, r >= 0);
+          copy16(st + L::kV + tok * L::RS + pc * 16, a.v_codes + vec * CB + pc * 16, r >= 0);
+        }
+        const int64_t vec = int64_t(row < 0 ? 0 : row) * a.heads + p.h;
+        const int kr = (lane & 16) | ((lane & 1) << 3) | ((lane & 15) >> 1);
+        const uint32_t dk = st + L::kKS + kr * L::SBS, dv = st + L::kVS + lane * L::SBS;
+        const uint16_t *ks = a.k_scales + vec * NG, *vs = a.v_scales + vec * NG;
+        if constexpr (L::SB >= 16) {
 #pragma unroll
-      for (int e = 0; e < EP; ++e) {
-        q[r][e] = a.qrot[v * D + lane * EP + e];
-        acc[r][e] = 0.0f;
-      }
-      m[r] = -INFINITY;
-      l[r] = 0.0f;
-    }
-    for (int t = t0 + warp; t < t1; t += NW) {
-      const int64_t row = a.map.row(table, uint32_t(t));
-      if (row < 0) continue;     // no page: the token is not there
-      const int64_t vec = row * a.heads + h;
-      const int gi = (lane * EP) >> a.lg_group;
-      float kv[EP], vv[EP];
-      lane_values<D, BITS>(a.k_codes + vec * CB, __half2float(__ushort_as_half(a.k_scales[vec * NG + gi])),
-                           lane, kv);
-      lane_values<D, BITS>(a.v_codes + vec * CB, __half2float(__ushort_as_half(a.v_scales[vec * NG + gi])),
-                           lane, vv);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < EP; ++e) s = fmaf(q[r][e], kv[e], s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (t < lim[r]) {
-          const float mn = fmaxf(m[r], s);
-          const float al = exp2f(m[r] - mn), p = exp2f(s - mn);
-          m[r] = mn;
-          l[r] = fmaf(l[r], al, p);
-#pragma unroll
-          for (int e = 0; e < EP; ++e) acc[r][e] = fmaf(acc[r][e], al, p * vv[e]);
+          for (int i = 0; i < L::SB / 16; ++i) {
+            copy16(dk + 16 * i, ks + 8 * i, row >= 0);
+            copy16(dv + 16 * i, vs + 8 * i, row >= 0);
+          }
+        } else if constexpr (L::SB >= 4) {
+          copy_small<L::SB>(dk, ks, row >= 0);
+          copy_small<L::SB>(dv, vs, row >= 0);
+        } else {   // one scale: 2 bytes, below the smallest asynchronous copy
+          uint8_t* sp = ws + (c % NS) * L::kStage;
+          *reinterpret_cast<uint16_t*>(sp + L::kKS + kr * L::SBS) = row >= 0 ? ks[0] : uint16_t(0);
+          *reinterpret_cast<uint16_t*>(sp + L::kVS + lane * L::SBS) = row >= 0 ? vs[0] : uint16_t(0);
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int32_t row_at[NS];   // rows of the chunks in flight, then of the next one
+#pragma unroll
+    for (int c = 0; c < NS; ++c) row_at[c] = row_of(c);
+#pragma unroll
+    for (int c = 0; c < NS - 1; ++c) issue(c, row_at[c]);
+
+    // this lane's part of query g: coordinates 16 s + 4 t .. + 3
+    const int rq = p.r0 + min(g, p.nr - 1);
+    const int bq = p.pre ? rq / qpk : p.b;
+    const float* qv = a.qrot + (int64_t(bq) * hq + p.h * qpk + (p.pre ? rq % qpk : rq)) * D;
+    float4 qf[S16];
+    float amax = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S16; ++s) {
+      qf[s] = __ldg(reinterpret_cast<const float4*>(qv + 16 * s + 4 * t));
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(qf[s].x), fabsf(qf[s].y)),
+                               fmaxf(fabsf(qf[s].z), fabsf(qf[s].w))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // 2^e with 2^e amax in [2^13, 2^14) (1 for a zero or infinite query)
+    const int ex = int((__float_as_uint(amax) >> 23) & 255u);
+    const int e = ex > 0 && ex < 255 ? min(max(140 - ex, -100), 100) : 0;
+    const float up = __uint_as_float(uint32_t(e + 127) << 23);
+    uint32_t qh[S16][2], ql[EXACT ? S16 : 1][2];
+    float gsum[NG];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) gsum[i] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S16; ++s) {
+      constexpr float odd = BITS == 4 ? 0.0625f : 1.0f;   // int4: odd coordinates' codes are 16 u
+      const float x0 = qf[s].x * up, x1 = qf[s].y * up, x2 = qf[s].z * up, x3 = qf[s].w * up;
+      qh[s][0] = pack_half2(x0, x2);
+      qh[s][1] = pack_half2(x1 * odd, x3 * odd);
+      float2 f0 = unpack_half2(qh[s][0]), f1 = unpack_half2(qh[s][1]);
+      if constexpr (EXACT) {
+        ql[s][0] = pack_half2(x0 - f0.x, x2 - f0.y);
+        ql[s][1] = pack_half2(x1 * odd - f1.x, x3 * odd - f1.y);
+        const float2 l0 = unpack_half2(ql[s][0]), l1 = unpack_half2(ql[s][1]);
+        f0 = make_float2(f0.x + l0.x, f0.y + l0.y);
+        f1 = make_float2(f1.x + l1.x, f1.y + l1.y);
+      }
+      gsum[16 * s / G] += (f0.x + f0.y) + (f1.x + f1.y) * (1.0f / odd);
+    }
+    // offsets of groups 2t, 2t + 1 (+ 8 i) as fp16 hi and lo: -(8 or 128) 2^-24 sum q
+    constexpr int NO = NG > 8 ? NG / 8 : 1;
+    uint32_t off[NO][2];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      gsum[i] += __shfl_xor_sync(0xffffffffu, gsum[i], 1);
+      gsum[i] += __shfl_xor_sync(0xffffffffu, gsum[i], 2);
+      gsum[i] *= BITS == 4 ? -0x1p-21f : -0x1p-17f;
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int o = 0; o < NO; ++o) {
+      float x0 = 0.0f, x1 = 0.0f;
 #pragma unroll
-      for (int e = 0; e < EP; ++e) acc_sh[warp][r][lane * EP + e] = acc[r][e];
-      if (lane == 0) ml_sh[warp][r] = make_float2(m[r], l[r]);
+      for (int i = 0; i < 8 && 8 * o + i < NG; ++i) {
+        if (i / 2 == t) (i % 2 ? x1 : x0) = gsum[8 * o + i];
+      }
+      off[o][0] = pack_half2(x0, x1);
+      off[o][1] = half2_rest(x0, x1, off[o][0]);
+    }
+    // columns 2t and 2t + 1 of the score tile: their factor, token limit
+    const float down = __uint_as_float(uint32_t(127 - e) << 23) * 0x1p24f;
+    const int lim_g = a.len(bq);
+    float fs[2];
+    int lim[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      fs[c] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * c);
+      lim[c] = __shfl_sync(0xffffffffu, lim_g, 8 * t + 4 * c);
+    }
+
+    float O[S16][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < S16; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[s][i] = 0.0f;
+
+    for (int c = 0; c < n_chunks; ++c) {
+      const uint32_t here = __ballot_sync(0xffffffffu, row_at[0] >= 0);
+#pragma unroll
+      for (int i = 0; i + 1 < NS; ++i) row_at[i] = row_at[i + 1];
+      issue(c + NS - 1, row_at[NS - 2]);
+      row_at[NS - 1] = row_of(c + NS);
+      asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
+      __syncwarp();
+      const uint32_t st = ws_a + uint32_t(c % NS) * L::kStage;
+      const int tk = p.t0 + kTileChunk * (warp + NW * c);
+
+      // scores of the chunk's two tiles: rows g, g + 8 = tokens 2g, 2g + 1
+      float S[2][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint32_t k0 = st + L::kK + (16 * mt + g) * L::RS, k1 = k0 + 8 * L::RS;
+        const uint32_t s0 = st + L::kKS + (16 * mt + g) * L::SBS, s1 = s0 + 8 * L::SBS;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[mt][i] = 0.0f;
+#pragma unroll
+        for (int o = 0; o < NO; ++o) {
+          const uint32_t w0 = lds32(s0 + 16 * o + 4 * t), w1 = lds32(s1 + 16 * o + 4 * t);
+          mma_f16(S[mt], w0, w1, w0, w1, off[o][0], off[o][1]);
+        }
+        float sg0[NG], sg1[NG];
+#pragma unroll
+        for (int i = 0; i < (NG + 7) / 8; ++i) {
+          const uint4 u0 = lds128(s0 + 16 * i), u1 = lds128(s1 + 16 * i);
+          const uint32_t x0[4] = {u0.x, u0.y, u0.z, u0.w}, x1[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+          for (int k = 0; k < 8 && 8 * i + k < NG; ++k) {
+            const float2 f0 = unpack_half2(x0[k / 2]), f1 = unpack_half2(x1[k / 2]);
+            sg0[8 * i + k] = k % 2 ? f0.y : f0.x;
+            sg1[8 * i + k] = k % 2 ? f1.y : f1.x;
+          }
+        }
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < G / 16; ++i) {
+            const int s = gi * (G / 16) + i;
+            uint32_t a0, a1, a2, a3;
+            if constexpr (BITS == 4) {
+              const uint32_t sel = t & 1 ? 0x4342u : 0x4140u;
+              const uint32_t y0 = __byte_perm(lds32(k0 + 8 * s + 4 * (t >> 1)), 0u, sel);
+              const uint32_t y1 = __byte_perm(lds32(k1 + 8 * s + 4 * (t >> 1)), 0u, sel);
+              a0 = (y0 & 0x000F000Fu) ^ 0x00080008u;
+              a1 = (y1 & 0x000F000Fu) ^ 0x00080008u;
+              a2 = (y0 & 0x00F000F0u) ^ 0x00800080u;
+              a3 = (y1 & 0x00F000F0u) ^ 0x00800080u;
+            } else {
+              const uint32_t y0 = lds32(k0 + 16 * s + 4 * t), y1 = lds32(k1 + 16 * s + 4 * t);
+              a0 = (y0 & 0x00FF00FFu) ^ 0x00800080u;
+              a1 = (y1 & 0x00FF00FFu) ^ 0x00800080u;
+              a2 = ((y0 >> 8) & 0x00FF00FFu) ^ 0x00800080u;
+              a3 = ((y1 >> 8) & 0x00FF00FFu) ^ 0x00800080u;
+            }
+            mma_f16(acc, a0, a1, a2, a3, qh[s][0], qh[s][1]);
+            if constexpr (EXACT) mma_f16(acc, a0, a1, a2, a3, ql[s][0], ql[s][1]);
+          }
+          S[mt][0] = fmaf(sg0[gi], acc[0], S[mt][0]);
+          S[mt][1] = fmaf(sg0[gi], acc[1], S[mt][1]);
+          S[mt][2] = fmaf(sg1[gi], acc[2], S[mt][2]);
+          S[mt][3] = fmaf(sg1[gi], acc[3], S[mt][3]);
+        }
+      }
+      // scale, mask, running maximum (equal in the 8 lanes of a column)
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 16 * mt + 2 * g + (i >> 1);
+          const bool on = ((here >> tok) & 1u) && tk + tok < lim[i & 1];
+          S[mt][i] = on ? S[mt][i] * fs[i & 1] : -INFINITY;
+          mx[i & 1] = fmaxf(mx[i & 1], S[mt][i]);
+        }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+      }
+      const float mn0 = fmaxf(m[0], mx[0]), mn1 = fmaxf(m[1], mx[1]);
+      if (__any_sync(0xffffffffu, mn0 > m[0] || mn1 > m[1])) {
+        const float al0 = m[0] == -INFINITY ? 0.0f : ex2(m[0] - mn0);
+        const float al1 = m[1] == -INFINITY ? 0.0f : ex2(m[1] - mn1);
+        l[0] *= al0;
+        l[1] *= al1;
+#pragma unroll
+        for (int s = 0; s < S16; ++s) {
+          O[s][0] *= al0;
+          O[s][1] *= al1;
+          O[s][2] *= al0;
+          O[s][3] *= al1;
+        }
+        m[0] = mn0;
+        m[1] = mn1;
+      }
+      // p' = 2^15 e^{x - m}; without any token yet the reference is 0 and p' = 0
+      const float b0 = (m[0] == -INFINITY ? 0.0f : m[0]) - 15.0f;
+      const float b1 = (m[1] == -INFINITY ? 0.0f : m[1]) - 15.0f;
+      uint32_t ph[2][2], pl[2][2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p0 = ex2(S[mt][2 * r] - b0), p1 = ex2(S[mt][2 * r + 1] - b1);
+          const uint32_t h = pack_half2(p0, p1);
+          ph[mt][r] = movmatrix_trans(h);
+          if constexpr (EXACT) {
+            l[0] += p0;
+            l[1] += p1;
+            pl[mt][r] = movmatrix_trans(half2_rest(p0, p1, h));
+          } else {   // the sum of the weights as they are used
+            const float2 f = unpack_half2(h);
+            l[0] += f.x;
+            l[1] += f.y;
+          }
+        }
+      // values
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        // scales of tokens 4t .. 4t + 3 of the tile as (4t, 4t + 2), (4t + 1, 4t + 3)
+        uint32_t se[NG], so[NG];
+        const uint32_t sv = st + L::kVS + (16 * mt + 4 * t) * L::SBS;
+#pragma unroll
+        for (int i = 0; i < (NG + 7) / 8; ++i) {
+          const uint4 u0 = lds128(sv + 16 * i), u1 = lds128(sv + L::SBS + 16 * i);
+          const uint4 u2 = lds128(sv + 2 * L::SBS + 16 * i), u3 = lds128(sv + 3 * L::SBS + 16 * i);
+          const uint32_t x0[4] = {u0.x, u0.y, u0.z, u0.w}, x1[4] = {u1.x, u1.y, u1.z, u1.w};
+          const uint32_t x2[4] = {u2.x, u2.y, u2.z, u2.w}, x3[4] = {u3.x, u3.y, u3.z, u3.w};
+#pragma unroll
+          for (int k = 0; k < 8 && 8 * i + k < NG; ++k) {
+            se[8 * i + k] = __byte_perm(x0[k / 2], x2[k / 2], k % 2 ? 0x7632 : 0x5410);
+            so[8 * i + k] = __byte_perm(x1[k / 2], x3[k / 2], k % 2 ? 0x7632 : 0x5410);
+          }
+        }
+        const uint32_t vr = st + L::kV + (16 * mt + (lane & 15)) * L::RS;
+        auto weigh = [&](int s, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+          const uint32_t e0 = se[16 * s / G], o0 = so[16 * s / G];
+          a0 = hmul2(a0, e0);
+          a1 = hmul2(a1, e0);
+          a2 = hmul2(a2, o0);
+          a3 = hmul2(a3, o0);
+          mma_f16(O[s], a0, a1, a2, a3, ph[mt][0], ph[mt][1]);
+          if constexpr (EXACT) mma_f16(O[s], a0, a1, a2, a3, pl[mt][0], pl[mt][1]);
+        };
+        // fp16 1024 + u, or 1024 + 16 u, to c / 128 or 16 c / 128 (exact)
+        constexpr uint32_t k128 = 0x20002000u;                       // 2^-7
+        constexpr uint32_t o8 = 0xC808C808u, o128 = 0xC880C880u;     // -1032 / 128, -1152 / 128
+        if constexpr (BITS == 4) {
+#pragma unroll
+          for (int s = 0; s < S16; s += 2) {
+            uint32_t r[2];
+            ldmatrix_bytes_trans(r[0], r[1], vr + 8 * s);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t y = r[i] >> 8;
+              weigh(s + i, hfma2((r[i] & 0x000F000Fu) ^ 0x64086408u, k128, o8),
+                    hfma2((r[i] & 0x00F000F0u) ^ 0x64806480u, k128, o128),
+                    hfma2((y & 0x000F000Fu) ^ 0x64086408u, k128, o8),
+                    hfma2((y & 0x00F000F0u) ^ 0x64806480u, k128, o128));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < S16; ++s) {
+            uint32_t r0, r1;
+            ldmatrix_bytes_trans(r0, r1, vr + 16 * s);
+            weigh(s, hfma2((r0 & 0x00FF00FFu) ^ 0x64806480u, k128, o128),
+                  hfma2((r1 & 0x00FF00FFu) ^ 0x64806480u, k128, o128),
+                  hfma2(((r0 >> 8) & 0x00FF00FFu) ^ 0x64806480u, k128, o128),
+                  hfma2(((r1 >> 8) & 0x00FF00FFu) ^ 0x64806480u, k128, o128));
+          }
+        }
+      }
+      __syncwarp();   // every lane is done with the stage before it is refilled
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+
+    // the warp's state over its stages: (m, l) and O[query][coord]
+    float* wo = reinterpret_cast<float*>(ws);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
+    }
+    if (g == 0) {
+      ml_sh[warp][2 * t] = make_float2(m[0], l[0] * 0x1p-15f);
+      ml_sh[warp][2 * t + 1] = make_float2(m[1], l[1] * 0x1p-15f);
+    }
+#pragma unroll
+    for (int s = 0; s < S16; ++s) {
+      constexpr float f0 = 0x1p-8f, f1 = BITS == 4 ? 0x1p-12f : 0x1p-8f;   // 128 / 2^15 (/ 16)
+      if constexpr (BITS == 4) {   // rows g, g + 8: coordinates 2g, 2g + 1
+        float* o = wo + 2 * t * D + 16 * s + 2 * g;
+        *reinterpret_cast<float2*>(o) = make_float2(O[s][0] * f0, O[s][2] * f1);
+        *reinterpret_cast<float2*>(o + D) = make_float2(O[s][1] * f0, O[s][3] * f1);
+      } else {                     // coordinates g, g + 8
+        float* o = wo + 2 * t * D + 16 * s + g;
+        o[0] = O[s][0] * f0;
+        o[8] = O[s][2] * f1;
+        o[D] = O[s][1] * f0;
+        o[D + 8] = O[s][3] * f1;
+      }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nr * D; i += NW * 32) {
-      const int r = i / D, j = i % D;
+    float* to_acc = p.pre ? a.pre_acc : a.own_acc;
+    float2* to_ml = p.pre ? a.pre_ml : a.own_ml;
+    for (int i = threadIdx.x; i < p.nr * (D / 4); i += NW * 32) {
+      const int r = i / (D / 4), j = i % (D / 4);
       float mt = -INFINITY;
 #pragma unroll
       for (int w = 0; w < NW; ++w) mt = fmaxf(mt, ml_sh[w][r].x);
-      float lt = 0.0f, at = 0.0f;
+      float lt = 0.0f;
+      float4 at = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float mw = ml_sh[w][r].x;
-        const float c = mw == -INFINITY ? 0.0f : exp2f(mw - mt);
-        lt = fmaf(c, ml_sh[w][r].y, lt);
-        at = fmaf(c, acc_sh[w][r][j], at);
+        const float2 x = ml_sh[w][r];
+        const float f = x.x == -INFINITY ? 0.0f : ex2(x.x - mt);
+        const float4 v = reinterpret_cast<const float4*>(smem + w * L::kWarp)[r * (D / 4) + j];
+        lt = fmaf(f, x.y, lt);
+        at = make_float4(fmaf(f, v.x, at.x), fmaf(f, v.y, at.y), fmaf(f, v.z, at.z),
+                         fmaf(f, v.w, at.w));
       }
-      (pre ? a.pre_acc : a.own_acc)[(part + r) * D + j] = at;
-      if (j == 0) (pre ? a.pre_ml : a.own_ml)[part + r] = make_float2(mt, lt);
+      reinterpret_cast<float4*>(to_acc + (p.part + r) * D)[j] = at;
+      if (j == 0) to_ml[p.part + r] = make_float2(mt, lt);
     }
-    __syncthreads();
+    __syncthreads();   // the partial sums are read before the next item's copies land there
   }
 }
 
