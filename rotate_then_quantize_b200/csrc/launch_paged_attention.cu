@@ -6,6 +6,11 @@
 
 namespace srftq {
 
+// Query rows per KV head from which the prefix goes to the tcgen05 kernel: it
+// computes 128 rows whatever their number, the other kernel 8 at a time.
+constexpr int64_t kMmaMinRows = 24;
+constexpr int kMmaRows = 128;
+
 template <int D>
 int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t stream);
 
@@ -14,6 +19,7 @@ namespace {
 // Sizes of a call that the caller's workspace and the launches follow from:
 // host values only, none of them dependent on the sequences' lengths.
 struct PrefixShape {
+  bool mma;
   int32_t splits, per, chunk_goal;
   int64_t q_off, plan_off, start_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
 };
@@ -21,16 +27,30 @@ struct PrefixShape {
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
 PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int64_t prefix_len,
-                         int sms) {
+                         bool exact, int sms) {
   PrefixShape s{};
   const int64_t rows = n_seq * g;
-  const int64_t tiles = (rows + kPrefixRows - 1) / kPrefixRows * heads;
+  s.mma = prefix_len > 0 && rows >= kMmaMinRows;
   if (prefix_len > 0) {
-    // parts enough for four blocks per SM, of at least 64 tokens
-    int64_t n = (4 * int64_t(sms) + tiles - 1) / tiles;
+    // blocks of one wave, their row tiles, and the tokens' worth of a block's
+    // start and end; the number of parts with the least time on those terms
+    const int64_t slots = s.mma ? int64_t(sms) * (d <= 128 && !exact ? 2 : 1) : 4 * int64_t(sms);
+    const int64_t tile = s.mma ? kMmaRows : kPrefixRows;
+    const int64_t units = (rows + tile - 1) / tile * heads;
+    const int64_t over = s.mma ? 256 : 128;
+    int64_t best = 0, best_n = 1;
     const int64_t most = (prefix_len + 63) / 64;
-    n = n < 1 ? 1 : n > most ? most : n;
-    const int64_t per = ((prefix_len + n - 1) / n + 63) / 64 * 64;
+    for (int64_t waves = 1; waves <= 4; ++waves) {
+      int64_t n = waves * slots / units;
+      n = n < 1 ? 1 : n > most ? most : n;
+      const int64_t per = ((prefix_len + n - 1) / n + 63) / 64 * 64;
+      const int64_t cost = (units * n + slots - 1) / slots * (per + over);
+      if (best == 0 || cost < best) {
+        best = cost;
+        best_n = n;
+      }
+    }
+    const int64_t per = ((prefix_len + best_n - 1) / best_n + 63) / 64 * 64;
     s.per = int32_t(per);
     s.splits = int32_t((prefix_len + per - 1) / per);
   }
@@ -57,12 +77,16 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
 
 int64_t prefix_attention_workspace(int32_t d, int32_t heads, int64_t n_seq, int32_t q_per_kv,
                                    int64_t prefix_len) {
-  return prefix_shape(d, heads, n_seq, q_per_kv, prefix_len, Runtime::num_sms()).bytes;
+  const int sms = Runtime::num_sms();
+  const int64_t x = prefix_shape(d, heads, n_seq, q_per_kv, prefix_len, false, sms).bytes;
+  const int64_t y = prefix_shape(d, heads, n_seq, q_per_kv, prefix_len, true, sms).bytes;
+  return x > y ? x : y;
 }
 
 int launch_prefix_attention(const PrefixAttnCall& c) {
   const int sms = Runtime::num_sms();
-  const PrefixShape s = prefix_shape(c.d, c.heads, c.n_seq, c.q_per_kv, c.prefix_len, sms);
+  const PrefixShape s =
+      prefix_shape(c.d, c.heads, c.n_seq, c.q_per_kv, c.prefix_len, !c.bf16, sms);
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   PrefixArgs a{};
   a.n_seq = int32_t(c.n_seq);
@@ -71,6 +95,7 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
   a.lg_group = ilog2(c.group);
   a.prefix_len = int32_t(c.prefix_len);
   a.max_pages = int32_t(c.max_pages);
+  a.pre_mma = s.mma;
   a.prefix_splits = s.splits;
   a.prefix_per = s.per;
   a.chunk_goal = s.chunk_goal;
@@ -98,9 +123,11 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
   a.pre_acc = reinterpret_cast<float*>(ws + s.pre_acc_off);
   a.own_ml = reinterpret_cast<float2*>(ws + s.own_ml_off);
   a.own_acc = reinterpret_cast<float*>(ws + s.own_acc_off);
+  a.guard = Runtime::guard_word();
+  if (!a.guard) return SRFTQ_ERR_CUDA;
   const int64_t queries = c.n_seq * c.heads * c.q_per_kv;
   const int64_t blocks = (queries + 7) / 8;   // a warp per query
-  if (blocks > INT_MAX) return SRFTQ_ERR_UNSUPPORTED;
+  if (queries > INT_MAX) return SRFTQ_ERR_UNSUPPORTED;
   int rc = SRFTQ_ERR_UNSUPPORTED;
   static_for<6, 9>([&](auto lg_) {
     constexpr int D = 1 << decltype(lg_)::value;
@@ -110,8 +137,8 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
     else prefix_prepare_kernel<kSRHT, D><<<g1, 256, 0, c.stream>>>(a);
     rc = launch_prefix_tiles<D>(a, c.bits, c.group, c.stream);
     if (rc != SRFTQ_OK) return;
-    if (c.rotation == kSRFT) prefix_merge_kernel<kSRFT, D><<<int(blocks), 256, 0, c.stream>>>(a);
-    else prefix_merge_kernel<kSRHT, D><<<int(blocks), 256, 0, c.stream>>>(a);
+    if (c.rotation == kSRFT) prefix_merge_kernel<kSRFT, D><<<int(queries), 32 * kMergeWarps, 0, c.stream>>>(a);
+    else prefix_merge_kernel<kSRHT, D><<<int(queries), 32 * kMergeWarps, 0, c.stream>>>(a);
     rc = finish_launch();
   });
   return rc;

@@ -4,9 +4,12 @@
 
 #include "launch_impl.cuh"
 #include "paged_attention.cuh"
+#include "prefix_mma.cuh"
 
 namespace srftq {
 
+// The own tokens' parts, and the prefix's: those either by the same kernel or,
+// before it, by the tcgen05 kernel (a.pre_mma).
 template <int D>
 int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t stream) {
   int rc = SRFTQ_ERR_UNSUPPORTED;
@@ -20,6 +23,13 @@ int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t s
         constexpr auto K = prefix_tile_kernel<D, BITS, G, EXACT>;
         constexpr int smem = TileLayout<D, BITS, G>::kBytes;
         int bps = 0;
+        if (a.pre_mma) {
+          using L = PrefixMma<D, BITS, G, EXACT>;
+          constexpr auto KM = prefix_mma_kernel<D, BITS, G, EXACT>;
+          if ((rc = prepare_smem<KM>(L::kSmem)) != SRFTQ_OK) return;
+          const int64_t tiles = (int64_t(a.n_seq) * a.q_per_kv + kMmaRows - 1) / kMmaRows;
+          KM<<<unsigned(tiles * a.heads * a.prefix_splits), L::kThreads, L::kSmem, stream>>>(a);
+        }
         rc = prepare_kernel<K>(smem, kTileWarps * 32, &bps);
         if (rc != SRFTQ_OK) return;
         K<<<Runtime::num_sms() * bps, kTileWarps * 32, smem, stream>>>(a);

@@ -20,7 +20,7 @@
 //                           log2 e into the workspace; block 0 also plans the
 //                           split of the sequences' own tokens;
 //   prefix_tile_kernel      the parts, each (m, l, a) into the workspace;
-//   prefix_merge_kernel     a warp per query head: joins its parts, applies
+//   prefix_merge_kernel     a block per query head: joins its parts, applies
 //                           lambda_V / l, R_V^T and s_V, rounds once.
 #pragma once
 
@@ -68,6 +68,7 @@ struct PrefixArgs {
   float scale;
   void* out;                           // like q
   float* lse;                          // [n_seq][heads q_per_kv] or null
+  bool pre_mma;                        // the prefix's parts come from prefix_mma_kernel
   float* qrot;                         // workspace: rotated queries
   PrefixPlan* plan;
   int32_t* chunk_start;
@@ -75,6 +76,7 @@ struct PrefixArgs {
   float* pre_acc;                      // the same rows of d
   float2* own_ml;                      // [chunks][heads][q_per_kv]
   float* own_acc;
+  unsigned* guard;
 
   // tokens of sequence b: all, those of its own
   __device__ __forceinline__ int32_t len(int b) const {
@@ -345,7 +347,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
   const uint32_t ws_a = smem_addr(ws);
   const int qpk = a.q_per_kv, hq = a.heads * qpk;
   const int M = a.n_seq * qpk;
-  const int pre_tiles = a.prefix_len > 0 ? (M + kPrefixRows - 1) / kPrefixRows : 0;
+  const int pre_tiles =
+      a.prefix_len > 0 && !a.pre_mma ? (M + kPrefixRows - 1) / kPrefixRows : 0;
   const int64_t n_pre = int64_t(a.prefix_splits) * a.heads * pre_tiles;
   const int own_tiles = (qpk + kPrefixRows - 1) / kPrefixRows;
   const int64_t n_items = n_pre + int64_t(a.plan->n_chunks) * a.heads * own_tiles;
@@ -718,48 +721,81 @@ __global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
   }
 }
 
+// A block per query head: the parts' (m, l) by all threads, then their
+// weighted sums a warp per part in turn, added over the warps in order, and
+// the rotation by the first warp.
+constexpr int kMergeWarps = 4;
+
 template <int ROT, int D>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixArgs a) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixArgs a) {
+  constexpr int E = D / 64, NW = kMergeWarps;
+  __shared__ float acc_sh[NW][D];
+  __shared__ float2 ml_sh[NW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = a.q_per_kv, hq = a.heads * g;
-  const int64_t total = int64_t(a.n_seq) * hq;
-  const int64_t v = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (v >= total) return;
+  const int64_t v = blockIdx.x;
   const int b = int(v / hq), h = int(v % hq) / g, j = int(v % hq) % g;
   const int64_t M = int64_t(a.n_seq) * g;
-  float m = -INFINITY, l = 0.0f;
+  const int n_pre = a.prefix_len > 0 && a.len(b) > 0 ? a.prefix_splits : 0;
+  const int c0 = a.chunk_start[b], n = n_pre + a.chunk_start[b + 1] - c0;
+  // parts 0 .. n_pre - 1 of the prefix, then the sequence's own
+  auto row_of = [&](int i) {
+    return i < n_pre ? (int64_t(i) * a.heads + h) * M + int64_t(b) * g + j
+                     : (int64_t(c0 + i - n_pre) * a.heads + h) * g + j;
+  };
+  auto ml_of = [&](int i) { return (i < n_pre ? a.pre_ml : a.own_ml)[row_of(i)]; };
+  // a part without tokens has l = 0 (a NaN goes on)
+  float m = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += NW * 32) m = fmaxf(m, ml_of(i).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) ml_sh[warp].x = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) m = fmaxf(m, ml_sh[w].x);
+  const float ref = m == -INFINITY ? 0.0f : m;
+
+  float l = 0.0f;
   float2 acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = make_float2(0.0f, 0.0f);
-  auto join = [&](float2 ml, const float* src) {
-    if (!(ml.y > 0.0f || ml.y != ml.y)) return;   // a part without tokens (a NaN goes on)
-    const float mn = fmaxf(m, ml.x);
-    const float c0 = m == -INFINITY ? 0.0f : exp2f(m - mn), c1 = exp2f(ml.x - mn);
-    m = mn;
-    l = l * c0 + ml.y * c1;
+#pragma unroll 4
+  for (int i = warp; i < n; i += NW) {
+    const int64_t r = row_of(i);
+    const float2 ml = (i < n_pre ? a.pre_ml : a.own_ml)[r];
+    const float2* src = reinterpret_cast<const float2*>((i < n_pre ? a.pre_acc : a.own_acc) + r * D);
+    float2 x[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 x = reinterpret_cast<const float2*>(src)[warp_pair<ROT, D>(lane, e)];
-      acc[e] = make_float2(acc[e].x * c0 + x.x * c1, acc[e].y * c0 + x.y * c1);
-    }
-  };
-  if (a.len(b) > 0 && a.prefix_len > 0) {
-    for (int s = 0; s < a.prefix_splits; ++s) {
-      const int64_t i = (int64_t(s) * a.heads + h) * M + int64_t(b) * g + j;
-      join(a.pre_ml[i], a.pre_acc + i * D);
+    for (int e = 0; e < E; ++e) x[e] = src[lane + 32 * e];
+    if (ml.y > 0.0f || ml.y != ml.y) {
+      const float c = exp2f(ml.x - ref);
+      l = fmaf(ml.y, c, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        acc[e] = make_float2(fmaf(x[e].x, c, acc[e].x), fmaf(x[e].y, c, acc[e].y));
     }
   }
-  for (int c = a.chunk_start[b]; c < a.chunk_start[b + 1]; ++c) {
-    const int64_t i = (int64_t(c) * a.heads + h) * g + j;
-    join(a.own_ml[i], a.own_acc + i * D);
-  }
+  if (lane == 0) ml_sh[warp].y = l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) reinterpret_cast<float2*>(acc_sh[warp])[lane + 32 * e] = acc[e];
+  __syncthreads();
+  if (warp > 0) return;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) l += ml_sh[w].y;
   const float inv = l > 0.0f ? 1.0f / l : l;   // no token: 0 (a NaN stays)
   const float2* lam = reinterpret_cast<const float2*>(a.v_lambda + int64_t(h) * D);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const float2 f = lam[warp_pair<ROT, D>(lane, e)];
-    acc[e] = make_float2(acc[e].x * inv * f.x, acc[e].y * inv * f.y);
+    const int k = warp_pair<ROT, D>(lane, e);
+    const float2 f = lam[k];
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float2 x = reinterpret_cast<const float2*>(acc_sh[w])[k];
+      s = make_float2(s.x + x.x, s.y + x.y);
+    }
+    acc[e] = make_float2(s.x * inv * f.x, s.y * inv * f.y);
   }
   warp_rotate_inverse<ROT, D>(acc, lane);
   const int8_t* sg = a.v_signs + int64_t(h) * D + 2 * E * lane;

@@ -54,8 +54,19 @@ def rows_of(table, tokens, page, n_pages):
     return np.where((p >= 0) & (p < n_pages), p * page + tokens % page, -1)
 
 
-def attention(q, khat, vhat, block_table, seq_lens, prefix_table, prefix_len, page, scale):
-    """(out, lse) in 64 bits; khat, vhat [rows, H, d] dequantised pools."""
+def attention(q, khat, vhat, block_table, seq_lens, prefix_table, prefix_len, page, scale,
+              spread=None):
+    """(out, lse) in 64 bits; khat, vhat [rows, H, d] dequantised pools.
+
+    spread, a [n_seq, HQ, 1] array, gets the standard deviation that the fp16
+    roundings inside give a coordinate of each row, to first order. With e_t the
+    error of score t and f_t, g_t the relative ones of weight and value, the
+    output moves by sum_t p_t (e_t (v_t - out) + (f_t + g_t) v_t). The errors
+    are independent; f, g have standard deviation u / sqrt 3 at most, e_t that
+    times the root of scale^2 sum_j 2 (q_j k_tj)^2 (key and query), which in the
+    rotated domain is 2 scale^2 |q|^2 |k_t|^2 / d, up to 1 + 2 cos^2(q, k_t) for
+    a key along the query: 1.5 covers cosines up to 0.5. R is orthogonal, so a
+    coordinate's share of the squared error is the row's over d."""
     n_seq, HQ, d = q.shape
     H = khat.shape[1]
     g = HQ // H
@@ -76,7 +87,15 @@ def attention(q, khat, vhat, block_table, seq_lens, prefix_table, prefix_len, pa
             m = s.max()
             p = np.exp(s - m)
             lse[b, hq] = m + np.log(p.sum())
-            out[b, hq] = p @ vhat[rows, hq // g] / p.sum()
+            v = vhat[rows, hq // g]
+            out[b, hq] = p @ v / p.sum()
+            if spread is not None:
+                k = khat[rows, hq // g]
+                qn = np.linalg.norm(np.asarray(q[b, hq], np.float64))
+                e2 = 1.5 * 2 * (scale * qn) ** 2 * (k * k).sum(-1) / d
+                part = e2 * ((v - out[b, hq]) ** 2).sum(-1) + 2 * (v * v).sum(-1)
+                w2 = (p / p.sum()) ** 2
+                spread[b, hq] = U / np.sqrt(3) * np.sqrt(w2 @ part / d)
     return out, lse
 
 
