@@ -21,7 +21,7 @@ namespace {
 struct PrefixShape {
   bool mma;
   int32_t splits, per, chunk_goal;
-  int64_t q_off, plan_off, start_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
+  int64_t q_off, image_off, factor_off, plan_off, start_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
 };
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -63,6 +63,9 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
     return at;
   };
   s.q_off = take(n_seq * heads * g * d * 4);
+  const int64_t padded = s.mma ? (rows + kMmaRows - 1) / kMmaRows * kMmaRows * heads : 0;
+  s.image_off = take(padded * d * 2 * (exact ? 2 : 1));
+  s.factor_off = take(padded * 4);
   s.plan_off = take(sizeof(PrefixPlan));
   s.start_off = take((n_seq + 1) * 4);
   s.pre_ml_off = take(s.splits * heads * rows * 8);
@@ -116,7 +119,10 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
   a.scale = c.scale;
   a.out = c.out;
   a.lse = c.lse;
+  a.bits = c.bits;
   a.qrot = reinterpret_cast<float*>(ws + s.q_off);
+  a.q_image = ws + s.image_off;
+  a.q_factor = reinterpret_cast<float*>(ws + s.factor_off);
   a.plan = reinterpret_cast<PrefixPlan*>(ws + s.plan_off);
   a.chunk_start = reinterpret_cast<int32_t*>(ws + s.start_off);
   a.pre_ml = reinterpret_cast<float2*>(ws + s.pre_ml_off);

@@ -69,7 +69,10 @@ struct PrefixArgs {
   void* out;                           // like q
   float* lse;                          // [n_seq][heads q_per_kv] or null
   bool pre_mma;                        // the prefix's parts come from prefix_mma_kernel
+  int32_t bits;
   float* qrot;                         // workspace: rotated queries
+  uint8_t* q_image;                    // pre_mma: the rows' fp16 tiles, [heads][tiles] of them
+  float* q_factor;                     // and the rows' score factors, [heads][tiles * 128]
   PrefixPlan* plan;
   int32_t* chunk_start;
   float2* pre_ml;                      // [splits][heads][n_seq q_per_kv]
@@ -139,6 +142,44 @@ __device__ inline void plan_own_tokens(const PrefixArgs& a) {
   }
 }
 
+// e with 2^e amax in [2^13, 2^14); 0 for a zero or infinite query.
+__device__ __forceinline__ int query_exponent(float amax) {
+  const int ex = int((__float_as_uint(amax) >> 23) & 255u);
+  return ex > 0 && ex < 255 ? min(max(140 - ex, -100), 100) : 0;
+}
+
+// Row r of head h in the fp16 tiles that the tcgen05 kernel copies to shared
+// memory as they are: tiles of 128 rows, each (for fp16 outputs) followed by the
+// rests; a tile is d / 64 pieces of rows of 128 bytes whose 16-byte chunks are
+// XOR-swizzled by the row. The 8 coordinates of a chunk lie in the order that
+// decoding the codes gives (prefix_mma.cuh: decoded_coord), odd ones over 16 for
+// int4, whose odd codes come out 16 times too large.
+template <int D>
+struct QueryRow {
+  uint8_t* p;
+  float* factor;
+  int r;
+  bool exact, four;
+  __device__ __forceinline__ QueryRow(const PrefixArgs& a, int h, int row) {
+    exact = !a.bf16;
+    four = a.bits == 4;
+    const int tiles = (a.n_seq * a.q_per_kv + 127) / 128;
+    const int64_t tile = int64_t(h) * tiles + row / 128;
+    r = row % 128;
+    p = a.q_image + tile * (256 * D * (exact ? 2 : 1));
+    factor = a.q_factor + tile * 128 + r;
+  }
+  __device__ __forceinline__ void put(int c, float x) const {
+    const int at = four ? (c & 3) * 2 + ((c >> 2) & 1)
+                        : (c & 4) + (c & 1) * 2 + ((c >> 1) & 1);
+    if (four && (c & 1)) x *= 0.0625f;
+    uint8_t* q = p + (c >> 6) * 16384 + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + at * 2;
+    const __half hi = __float2half_rn(x);
+    *reinterpret_cast<__half*>(q) = hi;
+    if (exact) *reinterpret_cast<__half*>(q + 256 * D) = __float2half_rn(x - __half2float(hi));
+  }
+};
+
 template <int ROT, int D>
 __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a) {
   constexpr int E = D / 64;
@@ -161,11 +202,39 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
     warp_rotate_forward<ROT, D>(z, lane);
     const float2* lam = reinterpret_cast<const float2*>(a.k_lambda + int64_t(h) * D);
     float2* o = reinterpret_cast<float2*>(a.qrot + v * D);
+    float amax = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int k = warp_pair<ROT, D>(lane, e);
       const float2 l = lam[k];
-      o[k] = make_float2(z[e].x * l.x * f, z[e].y * l.y * f);
+      z[e] = make_float2(z[e].x * l.x * f, z[e].y * l.y * f);
+      o[k] = z[e];
+      amax = fmaxf(amax, fmaxf(fabsf(z[e].x), fabsf(z[e].y)));
+    }
+    if (a.pre_mma) {
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, i));
+      const int e2 = query_exponent(amax);
+      const float up = __uint_as_float(uint32_t(e2 + 127) << 23);
+      const int b = int(v / hq), j = int(v % hq) % a.q_per_kv;
+      const int r = b * a.q_per_kv + j;
+      const QueryRow<D> row(a, h, r);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int k = warp_pair<ROT, D>(lane, e);
+        row.put(2 * k, z[e].x * up);
+        row.put(2 * k + 1, z[e].y * up);
+      }
+      if (lane == 0) *row.factor = __uint_as_float(uint32_t(127 - e2) << 23) * 128.0f;
+    }
+  }
+  if (a.pre_mma) {   // rows behind the last query: zeros
+    const int M = a.n_seq * a.q_per_kv, pad = (M + 127) / 128 * 128 - M;
+    for (int64_t v = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+         v < int64_t(pad) * a.heads; v += (int64_t(gridDim.x) * blockDim.x) >> 5) {
+      const QueryRow<D> row(a, int(v / pad), M + int(v % pad));
+      for (int c = lane; c < D; c += 32) row.put(c, 0.0f);
+      if (lane == 0) *row.factor = 1.0f;
     }
   }
   if (blockIdx.x == 0) plan_own_tokens(a);
@@ -426,9 +495,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // 2^e with 2^e amax in [2^13, 2^14) (1 for a zero or infinite query)
-    const int ex = int((__float_as_uint(amax) >> 23) & 255u);
-    const int e = ex > 0 && ex < 255 ? min(max(140 - ex, -100), 100) : 0;
+    const int e = query_exponent(amax);
     const float up = __uint_as_float(uint32_t(e + 127) << 23);
     uint32_t qh[S16][2], ql[EXACT ? S16 : 1][2];
     float gsum[NG];

@@ -45,9 +45,8 @@ struct PrefixMma {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQ * (EXACT ? 2 : 1);
   static constexpr int kVOff = kKOff + kStages * kKT;
-  static constexpr int kRowOff = kVOff + kStages * kT;        // float [128]: score factors
-  static constexpr int kOnOff = kRowOff + 4 * kMmaRows;       // uint32 [4 steps][2]: tokens there
-  static constexpr int kBarOff = kOnOff + 8 * 4;
+  static constexpr int kOnOff = kVOff + kStages * kT;         // uint8 [4 steps][TN]: tokens there
+  static constexpr int kBarOff = kOnOff + 4 * TN;
   static constexpr int kBytes = kBarOff + 8 * 20 + 16;
   static constexpr int kSmem = kBytes + 1024;                 // slack to start on 1024 bytes
   static constexpr int kThreads = 288;
@@ -100,12 +99,57 @@ __device__ __forceinline__ void decode_chunk(const uint32_t* w, uint32_t sg2, ui
   }
 }
 
+// A thread's NK pieces (16 bytes of codes, piece pc of rows tr, tr + RPP, ...) as
+// fp16 into a tile at `base` (rest_at > 0: their rests that far behind it). Chunks
+// of one row in different 128-byte columns share banks, so the threads of a store
+// start at different chunks (order j ^ rot).
+template <int D, int BITS, int G, int TN, bool REST, int NK>
+__device__ __forceinline__ void decode_pieces(uint32_t base, uint32_t rest_at, int pc, int tr,
+                                              const uint4 (&w)[NK], const uint32_t (&s)[NK]) {
+  constexpr int PPT = D * BITS / 128, RPP = 128 / PPT, NC = 16 / BITS;
+  constexpr bool TWO = 128 / BITS > G;   // two scales to a piece
+  const int rot = BITS == 4 ? (PPT == 4 ? (pc >> 1) * 2 : PPT == 8 ? pc >> 1 : 0)
+                            : (PPT >= 8 ? (pc >> 2) & 1 : 0);
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    const int tok = tr + k * RPP;
+    uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    uint32_t s0 = (TWO ? s[k] & 0xFFFFu : s[k]) * 0x10001u;
+    uint32_t s1 = TWO ? (s[k] >> 16) * 0x10001u : s0;
+    if (BITS == 8 ? rot & 1 : rot & 2) {
+      const uint32_t y0 = x[0], y1 = x[1], z = s0;
+      x[0] = x[2];
+      x[1] = x[3];
+      x[2] = y0;
+      x[3] = y1;
+      s0 = s1;
+      s1 = z;
+    }
+    if (BITS == 4 && (rot & 1)) {
+      const uint32_t y0 = x[0], y2 = x[2];
+      x[0] = x[1];
+      x[1] = y0;
+      x[2] = x[3];
+      x[3] = y2;
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = pc * NC + (j ^ rot);
+      const uint32_t at = base + (c >> 3) * (TN * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
+      uint4 v, r;
+      decode_chunk<BITS, REST>(x + j * 4 / NC, 2 * j < NC ? s0 : s1, v, r);
+      sts128(at, v);
+      if constexpr (REST) sts128(at + rest_at, r);
+    }
+  }
+}
+
 template <int D, int BITS, int G, bool EXACT>
 __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
                                   PrefixMma<D, BITS, G, EXACT>::kBlocks)
     prefix_mma_kernel(const PrefixArgs a) {
   using L = PrefixMma<D, BITS, G, EXACT>;
-  constexpr int TN = L::TN, CB = L::CB, NG = L::NG;
+  constexpr int TN = L::TN, CB = L::CB, NG = L::NG;   // tokens per step, code bytes, scales
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_a = smem_addr(smem_raw);
   uint8_t* smem = smem_raw + ((0u - raw_a) & 1023u);
@@ -114,10 +158,10 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6;
   uint64_t *sfull = bars + 8, *pfull = bars + 10, *odone = bars + 12, *drain = bars + 13;   // drain: all products done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 15);
-  float* row_f = reinterpret_cast<float*>(smem + L::kRowOff);
-  volatile uint32_t* on_sh = reinterpret_cast<volatile uint32_t*>(smem + L::kOnOff);
+  uint64_t* qfull = bars + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 16);
+  volatile uint8_t* on_sh = smem + L::kOnOff;
 
   // this block's head, rows and tokens
   const int g = a.q_per_kv, hq = a.heads * g, M = a.n_seq * g;
@@ -139,6 +183,7 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
     }
     mbar_init(odone, 1);
     mbar_init(drain, 1);
+    mbar_init(qfull, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -146,57 +191,19 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
-  // queries: a warp per row in turn, lane l its columns 4 l .. (+ 128 i)
-  for (int r = warp; r < kMmaRows; r += 9) {
-    const int rr = min(r0 + r, M - 1);
-    const float* qv = a.qrot + (int64_t(rr / g) * hq + h * g + rr % g) * D;
-    // decoded position 4 l .. 4 l + 3: half of a chunk of 8 coordinates
-    constexpr int NV = (D + 127) / 128;
-    float x[NV][4];
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int base = (128 * i + 4 * lane) & ~7, half = lane & 1;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c0 = decoded_coord<BITS>(k), c1 = decoded_coord<BITS>(4 + k);
-        x[i][k] = 128 * i + 4 * lane < D ? __ldg(qv + base + (half ? c1 : c0)) : 0.0f;
-        amax = fmaxf(amax, fabsf(x[i][k]));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int ex = int((__float_as_uint(amax) >> 23) & 255u);
-    const int e = ex > 0 && ex < 255 ? min(max(140 - ex, -100), 100) : 0;
-    const float up = __uint_as_float(uint32_t(e + 127) << 23);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = 128 * i + 4 * lane;
-      if (col >= D) continue;
-      float y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        y[k] = x[i][k] * up * (decoded_times16<BITS>(k) ? 0.0625f : 1.0f);
-      const uint2 hi = make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
-      // row r of piece col / 64: 16-byte chunk (col % 64) / 8, XOR-swizzled
-      const uint32_t at = sm + L::kQOff + (col >> 6) * L::kQPiece + r * 128 +
-                          ((((col & 63) >> 3) ^ (r & 7)) << 4) + (col & 4) * 2;
-      sts64(at, hi);
-      if constexpr (EXACT)
-        sts64(at + L::kQ, make_uint2(half2_rest(y[0], y[1], hi.x), half2_rest(y[2], y[3], hi.y)));
-    }
-    if (lane == 0) row_f[r] = __uint_as_float(uint32_t(127 - e) << 23) * 128.0f;
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int64_t tile = int64_t(h) * tiles + rt;
 
   if (warp == 8) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
-      bool ok = true;
+      constexpr uint32_t kQBytes = L::kQ * (EXACT ? 2 : 1);
+      mbar_arrive_expect_tx(qfull, kQBytes);
+      bulk_load(smem + L::kQOff, a.q_image + tile * kQBytes, kQBytes, qfull);
+      bool ok = wait_or_abort(qfull, 0, abort_flag, a.guard);
       auto values = [&](int i) {   // O += P(i) V(i)
         const int st = i & 1;
         if (!wait_or_abort(&vfull[st], (i >> 1) & 1, abort_flag, a.guard) ||
@@ -246,92 +253,89 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
     }
   } else if (warp >= 4) {
     // ---------------- codes to fp16 tiles ----------------
-    constexpr int TH = 128 / TN;                 // threads per token
-    constexpr int C = D / TH;                    // coordinates of a thread
-    constexpr int NB = C * BITS / 8, NV = NB / 16;
-    constexpr int GP = C > G ? C / G : 1;        // its scales
-    static_assert(NB % 16 == 0, "whole 16-byte pieces");
+    // Neighbouring threads take the 16-byte pieces of one row, so a load of a
+    // warp touches few lines; piece -> 16-byte chunks of 8 decoded coordinates.
+    constexpr int PPT = CB / 16, RPP = 128 / PPT;        // pieces of a row, rows per pass
+    constexpr int NK = TN / RPP;                         // pieces of a thread
+    constexpr int CC = 128 / BITS;                       // coordinates of a piece
+    constexpr int GC = CC > G ? CC / G : 1;              // its scales (1 or 2)
+    static_assert(TN % RPP == 0 && GC <= 2, "pieces");
     const int dt = tid - 128;
-    const int tok = dt % TN, part = dt / TN;     // token of the step, part of the row
-    const int sgi = part * C / G;
-    uint4 kw[NV], vw[NV];
-    uint16_t ks[GP], vs[GP];
-    auto row_at = [&](int i) {
-      const int t = t0 + i * TN + tok;
-      return i < n && t < t1 ? a.map.row(a.prefix_table, uint32_t(t)) : int64_t(-1);
+    const int pc = dt % PPT, tr = dt / PPT;
+    uint4 kw[NK], vw[NK];
+    uint32_t ks[NK], vs[NK];
+    int32_t page[NK], row[NK], next[NK];   // table entry two steps on; rows of this step, the next
+    auto token = [&](int i, int k) { return t0 + i * TN + tr + k * RPP; };
+    auto look_up = [&](int i, int k) {
+      const int t = token(i, k);
+      return i < n && t < t1 ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t))) : -1;
     };
-    auto load = [&](int64_t row, const uint8_t* codes, const uint16_t* scales, uint4 (&w)[NV],
-                    uint16_t (&s)[GP]) {
-      const int64_t vec = (row < 0 ? 0 : row) * a.heads + h;
+    auto row_at = [&](int i, int k, int32_t p) {
+      const uint32_t t = uint32_t(token(i, k));
+      return uint32_t(p) < uint32_t(a.map.n_pages)
+                 ? int32_t(uint32_t(p) * a.map.page.d + (t - a.map.page.div(t) * a.map.page.d))
+                 : -1;
+    };
+    auto load = [&](const int32_t (&r)[NK], const uint8_t* codes, const uint16_t* scales,
+                    uint4 (&w)[NK], uint32_t (&s)[NK]) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        w[k] = row < 0 ? make_uint4(0, 0, 0, 0)
-                       : __ldg(reinterpret_cast<const uint4*>(codes + vec * CB + part * NB) + k);
+      for (int k = 0; k < NK; ++k) {
+        const int64_t vec = int64_t(r[k] < 0 ? 0 : r[k]) * a.heads + h;
+        const uint16_t* sp = scales + vec * NG + pc * CC / G;
+        w[k] = make_uint4(0, 0, 0, 0);
+        s[k] = 0;
+        if (r[k] >= 0) {
+          w[k] = __ldg(reinterpret_cast<const uint4*>(codes + vec * CB) + pc);
+          s[k] = GC == 2 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : uint32_t(__ldg(sp));
+        }
+      }
+    };
 #pragma unroll
-      for (int k = 0; k < GP; ++k) s[k] = row < 0 ? uint16_t(0) : __ldg(scales + vec * NG + sgi + k);
-    };
-    // 16-byte chunk j of this thread's C coordinates in row `tok` of a tile
-    auto chunk_at = [&](uint32_t tile, int j) {
-      const int c = part * (C / 8) + j;
-      return tile + (c >> 3) * L::kTPiece + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
-    };
-    int64_t row = row_at(0), next = row_at(1);
-    if (n > 0) {
-      load(row, a.k_codes, a.k_scales, kw, ks);
-      load(row, a.v_codes, a.v_scales, vw, vs);
+    for (int k = 0; k < NK; ++k) {
+      row[k] = row_at(0, k, look_up(0, k));
+      next[k] = row_at(1, k, look_up(1, k));
     }
+    load(row, a.k_codes, a.k_scales, kw, ks);
+    load(row, a.v_codes, a.v_scales, vw, vs);
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
-      const int64_t after = row_at(i + 2);
+#pragma unroll
+      for (int k = 0; k < NK; ++k) page[k] = look_up(i + 2, k);
       if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&kempty[st], ((i >> 1) & 1) ^ 1,
                                                            abort_flag, a.guard)))
         break;
-      const uint32_t on = __ballot_sync(0xffffffffu, row >= 0);
-      // a slot is written again four steps on, after the scores of step i + 2,
-      // which follow the weights of this step
-      if (part == 0 && lane == 0) {
-        on_sh[2 * (i & 3) + (tok >> 5)] = on;
-        __threadfence_block();
-      }
-      const uint32_t kt = sm + L::kKOff + st * L::kKT;
+      // which tokens are there: bytes, written again four steps on, after the
+      // scores of step i + 2, which follow the weights of this step
+      if (pc == 0) {
 #pragma unroll
-      for (int j = 0; j < C / 8; ++j) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(kw) + j * BITS / 4;
-        const uint32_t s = ks[8 * j / G];
-        uint4 v, r;
-        decode_chunk<BITS, EXACT>(w, s | (s << 16), v, r);
-        sts128(chunk_at(kt, j), v);
-        if constexpr (EXACT) sts128(chunk_at(kt + L::kT, j), r);
+        for (int k = 0; k < NK; ++k) on_sh[(i & 3) * TN + tr + k * RPP] = row[k] >= 0 ? 1 : 0;
       }
+      decode_pieces<D, BITS, G, TN, EXACT, NK>(sm + L::kKOff + st * L::kKT, L::kT, pc, tr, kw, ks);
+      __threadfence_block();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&kfull[st]);
-      if (i + 1 < n) load(next, a.k_codes, a.k_scales, kw, ks);
+      load(next, a.k_codes, a.k_scales, kw, ks);
       if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&vempty[st], ((i >> 1) & 1) ^ 1,
                                                            abort_flag, a.guard)))
         break;
-      const uint32_t vt = sm + L::kVOff + st * L::kT;
-#pragma unroll
-      for (int j = 0; j < C / 8; ++j) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(vw) + j * BITS / 4;
-        const uint32_t s = vs[8 * j / G];
-        uint4 v, r;
-        decode_chunk<BITS, false>(w, s | (s << 16), v, r);
-        sts128(chunk_at(vt, j), v);
-      }
+      decode_pieces<D, BITS, G, TN, false, NK>(sm + L::kVOff + st * L::kT, 0, pc, tr, vw, vs);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&vfull[st]);
-      if (i + 1 < n) load(next, a.v_codes, a.v_scales, vw, vs);
-      row = next;
-      next = after;
+      load(next, a.v_codes, a.v_scales, vw, vs);
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        row[k] = next[k];
+        next[k] = row_at(i + 2, k, page[k]);
+      }
     }
   } else {
     // ---------------- softmax: a query row per thread ----------------
     const int r = tid;                       // row of the tile, lane of tensor memory
     const int rr = min(r0 + r, M - 1);
     const int lim = a.len(rr / g);
-    const float f = row_f[r];
+    const float f = a.q_factor[tile * kMmaRows + r];
     const uint32_t tl = tmem + (uint32_t(warp) << 21);   // lanes 32 warp ..
     float ref = -INFINITY, l = 0.0f;         // the reference of the weights, their sum
     bool ok = true;
@@ -349,14 +353,20 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
       if constexpr (TN == 64) tmem_wait_ld(s[0], s[TN / 32 - 1]);
       else tmem_wait_ld1(s[0]);
       const int tk = t0 + i * TN;
-      const uint32_t on0 = on_sh[2 * (i & 3)];
-      const uint32_t on1 = TN == 64 ? on_sh[2 * (i & 3) + 1] : 0xffffffffu;
-      if (!__all_sync(0xffffffffu, (on0 & on1) == 0xffffffffu && tk + TN <= lim)) {
+      // bit j of on[k]: token 32 k + j of the step is there
+      uint32_t on[TN / 32];
+      bool all = tk + TN <= lim;
+#pragma unroll
+      for (int k = 0; k < TN / 32; ++k) {
+        on[k] = __ballot_sync(0xffffffffu, on_sh[(i & 3) * TN + 32 * k + lane] != 0);
+        all = all && on[k] == 0xffffffffu;
+      }
+      if (!__all_sync(0xffffffffu, all)) {
 #pragma unroll
         for (int k = 0; k < TN / 32; ++k)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!(((k ? on1 : on0) >> j) & 1u) || tk + 32 * k + j >= lim) s[k][j] = 0xff800000u;
+            if (!((on[k] >> j) & 1u) || tk + 32 * k + j >= lim) s[k][j] = 0xff800000u;
       }
       float mx = -INFINITY;
 #pragma unroll
