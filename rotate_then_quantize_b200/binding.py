@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -434,30 +435,62 @@ def srftq_dequantize_dense(desc: SrftqDesc, codes, scales, operand, lam, xhat,
     _check("srftq_dequantize_dense", st)
 
 
-def _ints(t, dtype, shape: tuple, name: str):
-    """Address of a contiguous integer tensor of the given shape."""
+# The paged calls are made once per layer and step, so what they do on the host
+# is kept short: one look at the current device and stream per call, one
+# comparison per property of a tensor.
+_rt = None
+
+
+def _runtime():
+    """torch and the types of the paged calls, looked up once."""
+    global _rt
+    if _rt is None:
+        import types
+
+        import torch
+
+        _rt = types.SimpleNamespace(
+            torch=torch, F16=torch.float16, BF16=torch.bfloat16, F32=torch.float32,
+            U8=torch.uint8, I8=torch.int8, I32=torch.int32, I64=torch.int64,
+            get_device=getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+            raw_stream=getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    return _rt
+
+
+def _device(r) -> int:
+    """The current CUDA device (-2 without one: no tensor is there)."""
+    try:
+        return r.get_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _raw_stream(r, stream, dev: int) -> int:
+    if stream is not None or r.raw_stream is None:
+        return _stream_handle(stream)
+    return r.raw_stream(dev)
+
+
+def _address(t, dtype, shape: tuple, name: str, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _check_tensor(t, dtype, name)
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {list(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected contiguous {list(shape)}, got {tuple(t.shape)} with "
+                     f"strides {t.stride()}")
 
 
-def _vector(t, dtype, name: str):
-    """(address, length) of a contiguous one-dimensional tensor."""
-    _check_tensor(t, dtype, name)
-    if t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous vector, got {tuple(t.shape)}")
-    return t.data_ptr(), t.shape[0]
-
-
-def _pool(t, S: int, H: int, row_elems: int, name: str, dtype):
-    """(address, rows) of a contiguous [S, rows, H, e] pool."""
-    _check_tensor(t, dtype, name)
-    if (t.dim() != 4 or t.shape[0] != S or t.shape[2] != H or t.shape[3] != row_elems
-            or not t.is_contiguous()):
-        raise ValueError(f"{name}: expected contiguous [{S}, rows, {H}, {row_elems}], "
-                         f"got {tuple(t.shape)}")
-    return t.data_ptr(), t.shape[1]
+def _dims(t, n: int, name: str):
+    """The shape of a tensor of n dimensions."""
+    shape = getattr(t, "shape", None)
+    if shape is None or len(shape) != n:
+        raise ValueError(f"{name}: expected a tensor of {n} dimensions, got "
+                         f"{type(t).__name__ if shape is None else tuple(shape)}")
+    return shape
 
 
 def srftq_block_tables(cached_lens, new_lens, free_pages, block_table, page_size: int, slots,
@@ -465,45 +498,47 @@ def srftq_block_tables(cached_lens, new_lens, free_pages, block_table, page_size
     """Block tables and slot map of a step from the requests' lengths (see
     include/srftq.h): int32 tensors, slots int64; block_table [n_seq, max_pages]
     is extended in place, the last four are written."""
-    import torch
-
-    lib = load_library()
-    I32, I64 = torch.int32, torch.int64
-    pc, n_seq = _vector(cached_lens, I32, "cached_lens")
-    pf, n_free = _vector(free_pages, I32, "free_pages")
-    ps, n_slots = _vector(slots, I64, "slots")
-    _check_tensor(block_table, I32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != n_seq or not block_table.is_contiguous():
-        raise ValueError(f"block_table: expected contiguous [{n_seq}, max_pages], got "
-                         f"{tuple(block_table.shape)}")
-    st = lib.srftq_block_tables(n_seq, pc, _ints(new_lens, I32, (n_seq,), "new_lens"),
-                                int(page_size), pf, n_free, block_table.data_ptr(),
-                                block_table.shape[1], ps, n_slots,
-                                _ints(seq_lens, I32, (n_seq,), "seq_lens"),
-                                _ints(row_start, I32, (n_seq + 1,), "row_start"),
-                                _ints(counts, I32, (3,), "counts"), _stream_handle(stream))
+    lib, r = load_library(), _runtime()
+    I32, dev = r.I32, _device(r)
+    n_seq = _dims(cached_lens, 1, "cached_lens")[0]
+    n_free = _dims(free_pages, 1, "free_pages")[0]
+    n_slots = _dims(slots, 1, "slots")[0]
+    max_pages = _dims(block_table, 2, "block_table")[1]
+    st = lib.srftq_block_tables(
+        n_seq, _address(cached_lens, I32, (n_seq,), "cached_lens", dev),
+        _address(new_lens, I32, (n_seq,), "new_lens", dev), int(page_size),
+        _address(free_pages, I32, (n_free,), "free_pages", dev), n_free,
+        _address(block_table, I32, (n_seq, max_pages), "block_table", dev), max_pages,
+        _address(slots, r.I64, (n_slots,), "slots", dev), n_slots,
+        _address(seq_lens, I32, (n_seq,), "seq_lens", dev),
+        _address(row_start, I32, (n_seq + 1,), "row_start", dev),
+        _address(counts, I32, (3,), "counts", dev), _raw_stream(r, stream, dev))
     _check("srftq_block_tables", st)
+
+
+def _window(t, dtype, H: int, d: int, name: str, dev: int):
+    """(address, slices, rows, slice stride in rows) of [S, N, H, d] rows, or of a
+    window of a larger cache."""
+    S, N = _dims(t, 4, name)[:2]
+    if t.shape == (S, N, H, d) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr(), S, N, N
+    return _rows_view(t, H, d, name, dtype)
 
 
 def srftq_quantize_paged(desc: SrftqDesc, x, signs, lam, slots, codes, scales,
                          stream=None) -> None:
     """x [S,N,H,d] fp16 -> rows slots[r] (int64 [N]) of the pools codes
     [S,rows,H,d*bits/8] uint8 and scales [S,rows,H,d/G] fp16."""
-    lib = load_library()
-    F16, U8, I8, F32 = _dtypes()
-    import torch
-
-    H, d = desc.heads, desc.d
-    px, S, N, xs = _rows_view(x, H, d, "x", F16)
-    pc, rows = _pool(codes, S, H, d * desc.bits // 8, "codes", U8)
-    ps, rows2 = _pool(scales, S, H, d // desc.group, "scales", F16)
-    if rows2 != rows:
-        raise ValueError("codes and scales must have the same rows")
-    st = lib.srftq_quantize_paged(ctypes.byref(desc), S, N, px, xs,
-                                  _table(signs, S, H, d, "signs", I8),
-                                  _table(lam, S, H, d, "lambda", F32),
-                                  _ints(slots, torch.int64, (N,), "slots"), pc, ps, rows,
-                                  _stream_handle(stream))
+    lib, r = load_library(), _runtime()
+    H, d, dev = desc.heads, desc.d, _device(r)
+    px, S, N, xs = _window(x, r.F16, H, d, "x", dev)
+    rows = _dims(codes, 4, "codes")[1]
+    st = lib.srftq_quantize_paged(
+        ctypes.byref(desc), S, N, px, xs, _address(signs, r.I8, (S, H, d), "signs", dev),
+        _address(lam, r.F32, (S, H, d), "lambda", dev), _address(slots, r.I64, (N,), "slots", dev),
+        _address(codes, r.U8, (S, rows, H, d * desc.bits // 8), "codes", dev),
+        _address(scales, r.F16, (S, rows, H, d // desc.group), "scales", dev), rows,
+        _raw_stream(r, stream, dev))
     _check("srftq_quantize_paged", st)
 
 
@@ -511,21 +546,17 @@ def srftq_dequantize_paged(desc: SrftqDesc, codes, scales, slots, signs, lam, xh
                            stream=None) -> None:
     """Rows slots[r] of the pools -> rows r of xhat [S,N,H,d] fp16 (rows with a
     negative slot are left as they were)."""
-    lib = load_library()
-    F16, U8, I8, F32 = _dtypes()
-    import torch
-
-    H, d = desc.heads, desc.d
-    px, S, N, xs = _rows_view(xhat, H, d, "xhat", F16)
-    pc, rows = _pool(codes, S, H, d * desc.bits // 8, "codes", U8)
-    ps, rows2 = _pool(scales, S, H, d // desc.group, "scales", F16)
-    if rows2 != rows:
-        raise ValueError("codes and scales must have the same rows")
-    st = lib.srftq_dequantize_paged(ctypes.byref(desc), S, N, pc, ps, rows,
-                                    _ints(slots, torch.int64, (N,), "slots"),
-                                    _table(signs, S, H, d, "signs", I8),
-                                    _table(lam, S, H, d, "lambda", F32), px, xs,
-                                    _stream_handle(stream))
+    lib, r = load_library(), _runtime()
+    H, d, dev = desc.heads, desc.d, _device(r)
+    px, S, N, xs = _window(xhat, r.F16, H, d, "xhat", dev)
+    rows = _dims(codes, 4, "codes")[1]
+    st = lib.srftq_dequantize_paged(
+        ctypes.byref(desc), S, N,
+        _address(codes, r.U8, (S, rows, H, d * desc.bits // 8), "codes", dev),
+        _address(scales, r.F16, (S, rows, H, d // desc.group), "scales", dev), rows,
+        _address(slots, r.I64, (N,), "slots", dev),
+        _address(signs, r.I8, (S, H, d), "signs", dev),
+        _address(lam, r.F32, (S, H, d), "lambda", dev), px, xs, _raw_stream(r, stream, dev))
     _check("srftq_dequantize_paged", st)
 
 
@@ -547,51 +578,44 @@ def srftq_prefix_attention(desc: SrftqDesc, q, k_codes, k_scales, k_signs, k_lam
     each sequence, the first prefix_len tokens shared (see include/srftq.h).
     Pools are [rows, H, ...] tensors; prefix_table may be None for prefix_len 0,
     lse None; workspace is a contiguous uint8 tensor."""
-    import torch
-
-    lib = load_library()
-    F16, U8, I8, F32 = _dtypes()
-    H, d = desc.heads, desc.d
-    if not isinstance(q, torch.Tensor) or q.dtype not in (F16, torch.bfloat16):
-        raise ValueError("q: expected a float16 or bfloat16 tensor")
-    _check_tensor(q, q.dtype, "q")
-    if q.dim() != 3 or q.shape[1] % H or q.shape[2] != d or not q.is_contiguous():
-        raise ValueError(f"q: expected contiguous [n_seq, {H}*q_per_kv, {d}], got "
-                         f"{tuple(q.shape)}")
-    n_seq, q_per_kv = q.shape[0], q.shape[1] // H
-    _check_tensor(out, q.dtype, "out")
-    if out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor like q")
-    cb, ng = d * desc.bits // 8, d // desc.group
-    pk, rk = _cache_rows(k_codes, H, cb, "k_codes", U8)
-    pks, rks = _cache_rows(k_scales, H, ng, "k_scales", F16)
-    pv, rv = _cache_rows(v_codes, H, cb, "v_codes", U8)
-    pvs, rvs = _cache_rows(v_scales, H, ng, "v_scales", F16)
-    if not rk == rks == rv == rvs:
-        raise ValueError("the pools must have the same rows")
+    lib, r = load_library(), _runtime()
+    H, d, dev = desc.heads, desc.d, _device(r)
+    shape = _dims(q, 3, "q")
+    dtype = q.dtype
+    if dtype is not r.F16 and dtype is not r.BF16:
+        raise ValueError(f"q: expected float16 or bfloat16, got {dtype}")
+    n_seq, HQ = shape[0], shape[1]
+    if HQ % H:
+        raise ValueError(f"q: {HQ} heads are no multiple of the cache's {H}")
+    rows = _dims(k_codes, 3, "k_codes")[0]
     page_size, prefix_len = int(page_size), int(prefix_len)
-    if page_size < 1 or rk % page_size:
-        raise ValueError(f"the pools' {rk} rows are no whole pages of {page_size}")
-    pt, n_pt = (0, 0) if prefix_table is None else _vector(prefix_table, torch.int32,
-                                                           "prefix_table")
-    if n_pt * page_size < prefix_len:
-        raise ValueError(f"prefix_table: {n_pt} pages do not hold {prefix_len} tokens")
-    _check_tensor(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != n_seq or not block_table.is_contiguous():
-        raise ValueError(f"block_table: expected contiguous [{n_seq}, max_pages], got "
-                         f"{tuple(block_table.shape)}")
-    if lse is not None:
-        _check_tensor(lse, F32, "lse")
-        if lse.shape != q.shape[:2] or not lse.is_contiguous():
-            raise ValueError(f"lse: expected contiguous {list(q.shape[:2])}")
-    pw, n_ws = _vector(workspace, U8, "workspace")
+    if page_size < 1 or rows % page_size:
+        raise ValueError(f"the pools' {rows} rows are no whole pages of {page_size}")
+    codes_shape, scales_shape = (rows, H, d * desc.bits // 8), (rows, H, d // desc.group)
+    pt = 0
+    if prefix_table is not None:
+        n_pt = _dims(prefix_table, 1, "prefix_table")[0]
+        pt = _address(prefix_table, r.I32, (n_pt,), "prefix_table", dev)
+    if prefix_len > 0 and (prefix_table is None or n_pt * page_size < prefix_len):
+        raise ValueError(f"prefix_table: too few pages for {prefix_len} tokens")
+    max_pages = _dims(block_table, 2, "block_table")[1]
+    n_ws = _dims(workspace, 1, "workspace")[0]
     st = lib.srftq_prefix_attention(
-        ctypes.byref(desc), 0 if q.dtype == F16 else 1, n_seq, q_per_kv, q.data_ptr(), pk, pks,
-        _ints(k_signs, I8, (H, d), "k_signs"), _ints(k_lambda, F32, (H, d), "k_lambda"), pv, pvs,
-        _ints(v_signs, I8, (H, d), "v_signs"), _ints(v_lambda, F32, (H, d), "v_lambda"),
-        rk // page_size, page_size, pt, prefix_len, block_table.data_ptr(), block_table.shape[1],
-        _ints(seq_lens, torch.int32, (n_seq,), "seq_lens"), float(scale), out.data_ptr(),
-        None if lse is None else lse.data_ptr(), pw, n_ws, _stream_handle(stream))
+        ctypes.byref(desc), 0 if dtype is r.F16 else 1, n_seq, HQ // H,
+        _address(q, dtype, (n_seq, HQ, d), "q", dev),
+        _address(k_codes, r.U8, codes_shape, "k_codes", dev),
+        _address(k_scales, r.F16, scales_shape, "k_scales", dev),
+        _address(k_signs, r.I8, (H, d), "k_signs", dev),
+        _address(k_lambda, r.F32, (H, d), "k_lambda", dev),
+        _address(v_codes, r.U8, codes_shape, "v_codes", dev),
+        _address(v_scales, r.F16, scales_shape, "v_scales", dev),
+        _address(v_signs, r.I8, (H, d), "v_signs", dev),
+        _address(v_lambda, r.F32, (H, d), "v_lambda", dev), rows // page_size, page_size, pt,
+        prefix_len, _address(block_table, r.I32, (n_seq, max_pages), "block_table", dev),
+        max_pages, _address(seq_lens, r.I32, (n_seq,), "seq_lens", dev), float(scale),
+        _address(out, dtype, (n_seq, HQ, d), "out", dev),
+        None if lse is None else _address(lse, r.F32, (n_seq, HQ), "lse", dev),
+        _address(workspace, r.U8, (n_ws,), "workspace", dev), n_ws, _raw_stream(r, stream, dev))
     _check("srftq_prefix_attention", st)
 
 
@@ -771,12 +795,24 @@ def dequantize_dense(codes, scales, operand, lam, d: int, group: int = 16, bits:
     return xhat
 
 
-def _on(stream):
-    """Context in which torch allocates for work on `stream`: memory that the
-    call's end gives back is then reused in that stream's order."""
-    import torch
+@functools.lru_cache(maxsize=256)
+def _desc_of(d: int, heads: int, group: int, bits: int, rotation: int) -> SrftqDesc:
+    return make_desc(d, heads, group, bits, rotation)
 
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(d, heads, group, bits, rotation, n_seq, q_per_kv, prefix_len, device) -> int:
+    return srftq_prefix_attention_workspace(_desc_of(d, heads, group, bits, rotation), n_seq,
+                                            q_per_kv, prefix_len)
+
+
+def _empty(like, shape, dtype, stream):
+    """Memory for work on `stream`: what the call's end gives back is then reused
+    in that stream's order."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _runtime().torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def block_tables(cached_lens, new_lens, free_pages, block_table, page_size: int, n_slots: int,
@@ -786,14 +822,13 @@ def block_tables(cached_lens, new_lens, free_pages, block_table, page_size: int,
     counts [3]: pages taken, pages wanted, new tokens), the last three int32.
     n_slots is the batch's number of rows: those behind the last sequence's
     have slot -1."""
-    import torch
-
-    n_seq, dev = cached_lens.shape[0], cached_lens.device
-    with _on(stream):
-        slots = torch.empty(n_slots, dtype=torch.int64, device=dev)
-        seq_lens = torch.empty(n_seq, dtype=torch.int32, device=dev)
-        row_start = torch.empty(n_seq + 1, dtype=torch.int32, device=dev)
-        counts = torch.empty(3, dtype=torch.int32, device=dev)
+    r = _runtime()
+    n_seq = _dims(cached_lens, 1, "cached_lens")[0]
+    _check_tensor(cached_lens, r.I32, "cached_lens")
+    slots = _empty(cached_lens, n_slots, r.I64, stream)
+    seq_lens = _empty(cached_lens, n_seq, r.I32, stream)
+    row_start = _empty(cached_lens, n_seq + 1, r.I32, stream)
+    counts = _empty(cached_lens, 3, r.I32, stream)
     srftq_block_tables(cached_lens, new_lens, free_pages, block_table, page_size, slots, seq_lens,
                        row_start, counts, stream)
     return slots, seq_lens, row_start, counts
@@ -804,22 +839,24 @@ def quantize_paged(x, signs, lam, slots, codes, scales, group: int = 16, bits: i
     """Quantises x [S,N,H,d] fp16 into rows slots[r] of the pools codes
     [S,rows,H,d*bits/8] and scales [S,rows,H,d/group] (nowhere for a negative
     slot)."""
-    desc = make_desc(x.shape[3], x.shape[2], group, bits, rotation)
-    srftq_quantize_paged(desc, x, signs, lam, slots, codes, scales, stream)
+    _, _, H, d = _dims(x, 4, "x")
+    srftq_quantize_paged(_desc_of(d, H, group, bits, rotation), x, signs, lam, slots, codes,
+                         scales, stream)
 
 
 def dequantize_paged(codes, scales, slots, signs, lam, d: int, group: int = 16, bits: int = 4,
                      rotation: int = SRFT, out=None, stream=None):
     """Returns the rows slots[r] of the pools as fp16 [S,N,H,d]. Rows with a
     negative slot are left as they were in `out`, zero without one."""
-    import torch
-
-    S, _, H, _ = codes.shape
+    S, _, H, _ = _dims(codes, 4, "codes")
     if out is None:
-        with _on(stream):
-            out = torch.zeros((S, slots.shape[0], H, d), dtype=torch.float16, device=codes.device)
-    desc = make_desc(d, H, group, bits, rotation)
-    srftq_dequantize_paged(desc, codes, scales, slots, signs, lam, out, stream)
+        r = _runtime()
+        _check_tensor(codes, r.U8, "codes")
+        n = _dims(slots, 1, "slots")[0]
+        with contextlib.nullcontext() if stream is None else r.torch.cuda.stream(stream):
+            out = codes.new_zeros((S, n, H, d), dtype=r.F16)
+    srftq_dequantize_paged(_desc_of(d, H, group, bits, rotation), codes, scales, slots, signs, lam,
+                           out, stream)
     return out
 
 
@@ -832,24 +869,21 @@ def prefix_attention(q, k_codes, k_scales, k_signs, k_lambda, v_codes, v_scales,
     prefix_len tokens (see srftq_prefix_attention). Returns out [n_seq,
     H*q_per_kv, d] in q's type, or (out, lse) with the float32 log-sum-exp of
     the scores. Without a workspace it allocates one for the call."""
-    import math
-
-    import torch
-
-    n_seq, HQ, d = q.shape
-    H = k_codes.shape[1]
+    r = _runtime()
+    n_seq, HQ, d = _dims(q, 3, "q")
+    H = _dims(k_codes, 3, "k_codes")[1]
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    desc = make_desc(d, H, group, bits, rotation)
-    lse = None
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if return_lse:
-            lse = torch.empty((n_seq, HQ), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            need = srftq_prefix_attention_workspace(desc, n_seq, HQ // H, prefix_len)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        scale = d ** -0.5
+    desc = _desc_of(d, H, group, bits, rotation)
+    if out is None or workspace is None or return_lse:
+        _check_tensor(q, q.dtype, "q")
+    if out is None:
+        out = _empty(q, q.shape, q.dtype, stream)
+    lse = _empty(q, (n_seq, HQ), r.F32, stream) if return_lse else None
+    if workspace is None:
+        need = _workspace_bytes(d, H, group, bits, rotation, n_seq, HQ // H if H else 0,
+                                int(prefix_len), _device(r))
+        workspace = _empty(q, need, r.U8, stream)
     srftq_prefix_attention(desc, q, k_codes, k_scales, k_signs, k_lambda, v_codes, v_scales,
                            v_signs, v_lambda, page_size, prefix_table, prefix_len, block_table,
                            seq_lens, scale, out, lse, workspace, stream)

@@ -60,6 +60,11 @@ struct PrefixMma {
   static constexpr uint32_t kIdescO = f16_idesc<128, D>() | (1u << 16);   // B is MN-major
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Position p of 8 consecutive coordinates in the decoded order: the code pairs
 // that one AND isolates. int4: (0, 4), 16 (1, 5), (2, 6), 16 (3, 7); int8, two
 // words of 4: (0, 2), (1, 3) each.
@@ -368,12 +373,15 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
           for (int j = 0; j < 32; ++j)
             if (!((on[k] >> j) & 1u) || tk + 32 * k + j >= lim) s[k][j] = 0xff800000u;
       }
-      float mx = -INFINITY;
+      float mx = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int k = 0; k < TN / 32; ++k)
 #pragma unroll
-        for (int j = 0; j < 32; j += 2)
-          mx = fmaxf(mx, fmaxf(__uint_as_float(s[k][j]), __uint_as_float(s[k][j + 1])));
+        for (int j = 0; j < 32; j += 4) {
+          mx = max3(mx, __uint_as_float(s[k][j]), __uint_as_float(s[k][j + 1]));
+          mx1 = max3(mx1, __uint_as_float(s[k][j + 2]), __uint_as_float(s[k][j + 3]));
+        }
+      mx = fmaxf(mx, mx1);
       mx *= f;                               // f > 0
       const bool grow = mx > ref + 8.0f || (ref == -INFINITY && mx > -INFINITY);
       const float nref = grow ? mx : ref;
@@ -382,22 +390,24 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
       ref = nref;
       // P = 2^7 e^{x - ref} (0 while the row has seen no token)
       const float b = 7.0f - (ref == -INFINITY ? 0.0f : ref);
-      float sum = 0.0f, sum1 = 0.0f;
+      float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
       uint32_t ph[32];
       uint32_t pl[EXACT ? 32 : 1];
 #pragma unroll
       for (int k = 0; k < TN / 32; ++k)
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float p0 = ex2(fmaf(__uint_as_float(s[k][j]), f, b));
-          const float p1 = ex2(fmaf(__uint_as_float(s[k][j + 1]), f, b));
-          sum += p0;
-          sum1 += p1;
-          const uint32_t hh = pack_half2(p0, p1);
+          const float2 x = __ffma2_rn(
+              make_float2(__uint_as_float(s[k][j]), __uint_as_float(s[k][j + 1])),
+              make_float2(f, f), make_float2(b, b));
+          const float2 p = make_float2(ex2(x.x), ex2(x.y));
+          if (j & 2) sum1 = __fadd2_rn(sum1, p);
+          else sum = __fadd2_rn(sum, p);
+          const uint32_t hh = pack_half2(p.x, p.y);
           ph[16 * k + j / 2] = hh;
-          if constexpr (EXACT) pl[16 * k + j / 2] = half2_rest(p0, p1, hh);
+          if constexpr (EXACT) pl[16 * k + j / 2] = half2_rest(p.x, p.y, hh);
         }
-      l += sum + sum1;
+      l += (sum.x + sum.y) + (sum1.x + sum1.y);
       if constexpr (TN == 64) {
         tmem_st32(tl + st * L::kSCols, ph);
         if constexpr (EXACT) tmem_st32(tl + st * L::kSCols + 32, pl);
