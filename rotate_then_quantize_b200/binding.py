@@ -824,7 +824,8 @@ def block_tables(cached_lens, new_lens, free_pages, block_table, page_size: int,
     have slot -1."""
     r = _runtime()
     n_seq = _dims(cached_lens, 1, "cached_lens")[0]
-    _check_tensor(cached_lens, r.I32, "cached_lens")
+    if not isinstance(cached_lens, r.torch.Tensor):
+        _check_tensor(cached_lens, r.I32, "cached_lens")
     slots = _empty(cached_lens, n_slots, r.I64, stream)
     seq_lens = _empty(cached_lens, n_seq, r.I32, stream)
     row_start = _empty(cached_lens, n_seq + 1, r.I32, stream)
@@ -875,8 +876,8 @@ def prefix_attention(q, k_codes, k_scales, k_signs, k_lambda, v_codes, v_scales,
     if scale is None:
         scale = d ** -0.5
     desc = _desc_of(d, H, group, bits, rotation)
-    if out is None or workspace is None or return_lse:
-        _check_tensor(q, q.dtype, "q")
+    if not isinstance(q, r.torch.Tensor):
+        _check_tensor(q, None, "q")
     if out is None:
         out = _empty(q, q.shape, q.dtype, stream)
     lse = _empty(q, (n_seq, HQ), r.F32, stream) if return_lse else None

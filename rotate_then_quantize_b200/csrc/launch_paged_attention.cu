@@ -2,17 +2,17 @@
 #include <climits>
 
 #include "launch_impl.cuh"
-#include "paged_attention.cuh"
+#include "launch_prefix_tiles.cuh"
 
 namespace srftq {
 
 // Query rows per KV head from which the prefix goes to the tcgen05 kernel: it
 // computes 128 rows whatever their number, the other kernel 8 at a time.
-constexpr int64_t kMmaMinRows = 24;
-constexpr int kMmaRows = 128;
+constexpr int64_t kMmaMinRows = 24, kMmaMinRowsExact = 48;
 
-template <int D>
-int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t stream);
+extern template int launch_prefix_tiles<64>(const PrefixArgs&, int, int, cudaStream_t);
+extern template int launch_prefix_tiles<128>(const PrefixArgs&, int, int, cudaStream_t);
+extern template int launch_prefix_tiles<256>(const PrefixArgs&, int, int, cudaStream_t);
 
 namespace {
 
@@ -30,21 +30,20 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
                          bool exact, int sms) {
   PrefixShape s{};
   const int64_t rows = n_seq * g;
-  s.mma = prefix_len > 0 && rows >= kMmaMinRows;
+  s.mma = prefix_len > 0 && rows >= (exact ? kMmaMinRowsExact : kMmaMinRows);
   if (prefix_len > 0) {
-    // blocks of one wave, their row tiles, and the tokens' worth of a block's
-    // start and end; the number of parts with the least time on those terms
+    // blocks of one wave, their row tiles, and what a block's start and end and
+    // a part's join cost in tokens; the number of parts with the least time on
+    // those terms
     const int64_t slots = s.mma ? int64_t(sms) * (d <= 128 && !exact ? 2 : 1) : 4 * int64_t(sms);
     const int64_t tile = s.mma ? kMmaRows : kPrefixRows;
     const int64_t units = (rows + tile - 1) / tile * heads;
     const int64_t over = s.mma ? 256 : 128;
     int64_t best = 0, best_n = 1;
     const int64_t most = (prefix_len + 63) / 64;
-    for (int64_t waves = 1; waves <= 4; ++waves) {
-      int64_t n = waves * slots / units;
-      n = n < 1 ? 1 : n > most ? most : n;
+    for (int64_t n = 1; n <= most && units * n <= 4 * slots + units; n += n / 16 + 1) {
       const int64_t per = ((prefix_len + n - 1) / n + 63) / 64 * 64;
-      const int64_t cost = (units * n + slots - 1) / slots * (per + over);
+      const int64_t cost = (units * n + slots - 1) / slots * (per + over) + 4 * n;
       if (best == 0 || cost < best) {
         best = cost;
         best_n = n;
@@ -54,7 +53,7 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
     s.per = int32_t(per);
     s.splits = int32_t((prefix_len + per - 1) / per);
   }
-  s.chunk_goal = int32_t((8 * int64_t(sms) + heads - 1) / heads);
+  s.chunk_goal = int32_t((4 * int64_t(sms) + heads - 1) / heads);
   const int64_t chunks = s.chunk_goal + n_seq;
   int64_t o = 0;
   auto take = [&](int64_t bytes) {
@@ -143,8 +142,15 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
     else prefix_prepare_kernel<kSRHT, D><<<g1, 256, 0, c.stream>>>(a);
     rc = launch_prefix_tiles<D>(a, c.bits, c.group, c.stream);
     if (rc != SRFTQ_OK) return;
-    if (c.rotation == kSRFT) prefix_merge_kernel<kSRFT, D><<<int(queries), 32 * kMergeWarps, 0, c.stream>>>(a);
-    else prefix_merge_kernel<kSRHT, D><<<int(queries), 32 * kMergeWarps, 0, c.stream>>>(a);
+    // few query heads: more warps each, since then a block's own time counts
+    static_for<0, 2>([&](auto w_) {
+      constexpr int NW = decltype(w_)::value ? 16 : 4;
+      if ((queries <= 2 * sms) != (NW == 16)) return;
+      rc = c.rotation == kSRFT
+               ? launch_after<prefix_merge_kernel<kSRFT, D, NW>>(int(queries), 32 * NW, 0, c.stream, a)
+               : launch_after<prefix_merge_kernel<kSRHT, D, NW>>(int(queries), 32 * NW, 0, c.stream, a);
+    });
+    if (rc != SRFTQ_OK) return;
     rc = finish_launch();
   });
   return rc;

@@ -8,6 +8,27 @@
 
 namespace srftq {
 
+// A programmatic launch: the grid may start while the one before it on the
+// stream finishes, and waits for its results with griddepcontrol.wait.
+template <auto K>
+int launch_after(int grid, int threads, int smem, cudaStream_t stream, const PrefixArgs& a) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, K, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return SRFTQ_ERR_CUDA;
+  }
+  return SRFTQ_OK;
+}
+
 // The own tokens' parts, and the prefix's: those either by the same kernel or,
 // before it, by the tcgen05 kernel (a.pre_mma).
 template <int D>
@@ -28,12 +49,13 @@ int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t s
           constexpr auto KM = prefix_mma_kernel<D, BITS, G, EXACT>;
           if ((rc = prepare_smem<KM>(L::kSmem)) != SRFTQ_OK) return;
           const int64_t tiles = (int64_t(a.n_seq) * a.q_per_kv + kMmaRows - 1) / kMmaRows;
-          KM<<<unsigned(tiles * a.heads * a.prefix_splits), L::kThreads, L::kSmem, stream>>>(a);
+          rc = launch_after<KM>(int(tiles * a.heads * a.prefix_splits), L::kThreads, L::kSmem,
+                                stream, a);
+          if (rc != SRFTQ_OK) return;
         }
         rc = prepare_kernel<K>(smem, kTileWarps * 32, &bps);
         if (rc != SRFTQ_OK) return;
-        K<<<Runtime::num_sms() * bps, kTileWarps * 32, smem, stream>>>(a);
-        rc = finish_launch();
+        rc = launch_after<K>(Runtime::num_sms() * bps, kTileWarps * 32, smem, stream, a);
       });
     });
   });

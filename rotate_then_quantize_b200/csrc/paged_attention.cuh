@@ -15,7 +15,8 @@
 // below prefix_len are one part (or several) whose rows are the queries of all
 // sequences; the rest of each sequence are parts of its own.
 //
-// Three launches on the caller's stream:
+// Three launches on the caller's stream (four with prefix_mma.cuh), each but the
+// first a programmatic one:
 //   prefix_prepare_kernel   a warp per query: lambda_K * R_K (s_K q) * scale *
 //                           log2 e into the workspace; block 0 also plans the
 //                           split of the sequences' own tokens;
@@ -96,6 +97,15 @@ __device__ __forceinline__ float lo_f32(uint32_t w, bool bf16) {
 }
 __device__ __forceinline__ float hi_f32(uint32_t w, bool bf16) {
   return bf16 ? __uint_as_float(w & 0xFFFF0000u) : __half2float(__ushort_as_half(uint16_t(w >> 16)));
+}
+
+// Programmatic launches (launch_after): the next grid may start from here on;
+// the grids before this one are complete from here on.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Block-wide scan of the chunk counts (all threads of a block of 256).
@@ -183,6 +193,7 @@ struct QueryRow {
 template <int ROT, int D>
 __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a) {
   constexpr int E = D / 64;
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int hq = a.heads * a.q_per_kv;
   const int64_t total = int64_t(a.n_seq) * hq;
@@ -403,12 +414,14 @@ __device__ __forceinline__ PartItem pre_item(const PrefixArgs& a, int64_t i, int
 }
 
 template <int D, int BITS, int G, bool EXACT>
-__global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
+__global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
     prefix_tile_kernel(const PrefixArgs a) {
   using L = TileLayout<D, BITS, G>;
   constexpr int CB = L::CB, NG = L::NG, NS = L::kStages, S16 = L::NS16, NW = kTileWarps;
   constexpr int PPT = CB / 16;          // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
+  grid_launch_dependents();
+  grid_dependency_wait();
   float2(*ml_sh)[8] = reinterpret_cast<float2(*)[8]>(smem + L::kMl);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -626,12 +639,20 @@ __global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = 16 * mt + 2 * g + (i >> 1);
-          const bool on = ((here >> tok) & 1u) && tk + tok < lim[i & 1];
-          S[mt][i] = on ? S[mt][i] * fs[i & 1] : -INFINITY;
-          mx[i & 1] = fmaxf(mx[i & 1], S[mt][i]);
-        }
+        for (int i = 0; i < 4; ++i) S[mt][i] *= fs[i & 1];
+      if (here != 0xffffffffu || __any_sync(0xffffffffu, tk + kTileChunk > min(lim[0], lim[1]))) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tok = 16 * mt + 2 * g + (i >> 1);
+            if (!((here >> tok) & 1u) || tk + tok >= lim[i & 1]) S[mt][i] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i & 1] = fmaxf(mx[i & 1], S[mt][i]);
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
@@ -664,15 +685,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
           const float p0 = ex2(S[mt][2 * r] - b0), p1 = ex2(S[mt][2 * r + 1] - b1);
           const uint32_t h = pack_half2(p0, p1);
           ph[mt][r] = movmatrix_trans(h);
-          if constexpr (EXACT) {
-            l[0] += p0;
-            l[1] += p1;
-            pl[mt][r] = movmatrix_trans(half2_rest(p0, p1, h));
-          } else {   // the sum of the weights as they are used
-            const float2 f = unpack_half2(h);
-            l[0] += f.x;
-            l[1] += f.y;
-          }
+          l[0] += p0;
+          l[1] += p1;
+          if constexpr (EXACT) pl[mt][r] = movmatrix_trans(half2_rest(p0, p1, h));
         }
       // values
 #pragma unroll
@@ -791,11 +806,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, D <= 128 ? 3 : 2)
 // A block per query head: the parts' (m, l) by all threads, then their
 // weighted sums a warp per part in turn, added over the warps in order, and
 // the rotation by the first warp.
-constexpr int kMergeWarps = 4;
-
-template <int ROT, int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixArgs a) {
-  constexpr int E = D / 64, NW = kMergeWarps;
+template <int ROT, int D, int NW>
+__global__ void __launch_bounds__(NW * 32) prefix_merge_kernel(const PrefixArgs a) {
+  constexpr int E = D / 64;
+  grid_dependency_wait();
   __shared__ float acc_sh[NW][D];
   __shared__ float2 ml_sh[NW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

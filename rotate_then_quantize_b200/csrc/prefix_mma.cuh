@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_launch_dependents();
+  grid_dependency_wait();   // the query tiles
   const uint32_t tmem = *tmem_slot;
   const int64_t tile = int64_t(h) * tiles + rt;
 
