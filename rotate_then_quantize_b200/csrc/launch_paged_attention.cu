@@ -19,7 +19,7 @@ namespace {
 // Sizes of a call that the caller's workspace and the launches follow from:
 // host values only, none of them dependent on the sequences' lengths.
 struct PrefixShape {
-  bool mma;
+  bool mma, shared;   // parts by tcgen05; its two units different rows, not alternate tokens
   int32_t splits, per, chunk_goal;
   int64_t q_off, image_off, factor_off, plan_off, start_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
 };
@@ -35,10 +35,12 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
     // blocks of one wave, their row tiles, and what a block's start and end and
     // a part's join cost in tokens; the number of parts with the least time on
     // those terms
-    const int64_t slots = s.mma ? int64_t(sms) * (d <= 128 && !exact ? 2 : 1) : 4 * int64_t(sms);
-    const int64_t tile = s.mma ? kMmaRows : kPrefixRows;
+    s.shared = s.mma && d <= 128 && !exact && rows > kMmaRows;
+    const bool pair = s.mma && d <= 128 && !s.shared;   // a block makes two parts
+    const int64_t slots = s.mma ? sms : 4 * int64_t(sms);
+    const int64_t tile = s.shared ? 2 * kMmaRows : s.mma ? kMmaRows : kPrefixRows;
     const int64_t units = (rows + tile - 1) / tile * heads;
-    const int64_t over = s.mma ? 256 : 128;
+    const int64_t over = s.mma ? 512 : 128;
     int64_t best = 0, best_n = 1;
     const int64_t most = (prefix_len + 63) / 64;
     for (int64_t n = 1; n <= most && units * n <= 4 * slots + units; n += n / 16 + 1) {
@@ -51,7 +53,7 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
     }
     const int64_t per = ((prefix_len + best_n - 1) / best_n + 63) / 64 * 64;
     s.per = int32_t(per);
-    s.splits = int32_t((prefix_len + per - 1) / per);
+    s.splits = int32_t((prefix_len + per - 1) / per) * (pair ? 2 : 1);
   }
   s.chunk_goal = int32_t((4 * int64_t(sms) + heads - 1) / heads);
   const int64_t chunks = s.chunk_goal + n_seq;
@@ -98,6 +100,7 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
   a.prefix_len = int32_t(c.prefix_len);
   a.max_pages = int32_t(c.max_pages);
   a.pre_mma = s.mma;
+  a.pre_shared = s.shared;
   a.prefix_splits = s.splits;
   a.prefix_per = s.per;
   a.chunk_goal = s.chunk_goal;

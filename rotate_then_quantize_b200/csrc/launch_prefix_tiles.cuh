@@ -5,6 +5,7 @@
 #include "launch_impl.cuh"
 #include "paged_attention.cuh"
 #include "prefix_mma.cuh"
+#include "prefix_pair.cuh"
 
 namespace srftq {
 
@@ -29,6 +30,35 @@ int launch_after(int grid, int threads, int smem, cudaStream_t stream, const Pre
   return SRFTQ_OK;
 }
 
+// The prefix's parts on tcgen05: d = 256, whose accumulators fill the tensor
+// memory, by one unit per SM; else two units (a.pre_shared: of different rows).
+template <int D, int BITS, int G, bool EXACT>
+int launch_prefix_mma(const PrefixArgs& a, cudaStream_t stream) {
+  const int64_t M = int64_t(a.n_seq) * a.q_per_kv;
+  if constexpr (D == 256) {
+    using L = PrefixMma<D, BITS, G, EXACT>;
+    constexpr auto K = prefix_mma_kernel<D, BITS, G, EXACT>;
+    const int rc = prepare_smem<K>(L::kSmem);
+    if (rc != SRFTQ_OK) return rc;
+    const int64_t tiles = (M + kMmaRows - 1) / kMmaRows;
+    return launch_after<K>(int(tiles * a.heads * a.prefix_splits), L::kThreads, L::kSmem, stream, a);
+  } else {
+    int rc = SRFTQ_ERR_UNSUPPORTED;
+    static_for<0, EXACT ? 1 : 2>([&](auto s_) {
+      constexpr bool SHARED = decltype(s_)::value != 0;
+      if (a.pre_shared != SHARED) return;
+      using L = PrefixPair<D, BITS, G, EXACT, SHARED>;
+      constexpr auto K = prefix_pair_kernel<D, BITS, G, EXACT, SHARED>;
+      rc = prepare_smem<K>(L::kSmem);
+      if (rc != SRFTQ_OK) return;
+      const int64_t rows = SHARED ? 2 * kMmaRows : kMmaRows, blocks = (M + rows - 1) / rows;
+      const int parts = SHARED ? a.prefix_splits : a.prefix_splits / 2;
+      rc = launch_after<K>(int(blocks * a.heads * parts), L::kThreads, L::kSmem, stream, a);
+    });
+    return rc;
+  }
+}
+
 // The own tokens' parts, and the prefix's: those either by the same kernel or,
 // before it, by the tcgen05 kernel (a.pre_mma).
 template <int D>
@@ -45,12 +75,7 @@ int launch_prefix_tiles(const PrefixArgs& a, int bits, int group, cudaStream_t s
         constexpr int smem = TileLayout<D, BITS, G>::kBytes;
         int bps = 0;
         if (a.pre_mma) {
-          using L = PrefixMma<D, BITS, G, EXACT>;
-          constexpr auto KM = prefix_mma_kernel<D, BITS, G, EXACT>;
-          if ((rc = prepare_smem<KM>(L::kSmem)) != SRFTQ_OK) return;
-          const int64_t tiles = (int64_t(a.n_seq) * a.q_per_kv + kMmaRows - 1) / kMmaRows;
-          rc = launch_after<KM>(int(tiles * a.heads * a.prefix_splits), L::kThreads, L::kSmem,
-                                stream, a);
+          rc = launch_prefix_mma<D, BITS, G, EXACT>(a, stream);
           if (rc != SRFTQ_OK) return;
         }
         rc = prepare_kernel<K>(smem, kTileWarps * 32, &bps);

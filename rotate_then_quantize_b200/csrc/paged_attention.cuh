@@ -69,7 +69,8 @@ struct PrefixArgs {
   float scale;
   void* out;                           // like q
   float* lse;                          // [n_seq][heads q_per_kv] or null
-  bool pre_mma;                        // the prefix's parts come from prefix_mma_kernel
+  bool pre_mma;                        // the prefix's parts come from a tcgen05 kernel
+  bool pre_shared;                     // whose two units are different rows (prefix_pair.cuh)
   int32_t bits;
   float* qrot;                         // workspace: rotated queries
   uint8_t* q_image;                    // pre_mma: the rows' fp16 tiles, [heads][tiles] of them

@@ -1,0 +1,481 @@
+// Parts of the shared prefix on the 5th-generation tensor cores (tcgen05) for
+// d = 64 and 128: two units of 128 query rows on each SM.
+//
+// A unit is 128 query rows with a score tile S, weights P over it, and an
+// accumulator O, all in tensor memory, the rows' queries too:
+//   S[row][token]  = Q (sigma c / 128)^T      TN = 64 tokens at a time;
+//   P[row][token]  = 2^7 e^{x - ref}, fp16, written over S;
+//   O[row][coord] += P (sigma c / 128).
+// While one unit's four warps take exponentials the tensor cores form the other
+// unit's products, so the special function units always have work. Two forms:
+//   shared   the units are 256 different rows over the same tokens: a token's
+//            codes are decoded once for both (bf16 outputs, more than 128 rows);
+//   split    the units are the same rows over alternate tiles, two parts of the
+//            softmax (up to 128 rows, and fp16 outputs).
+// The left operands come from tensor memory and the right ones, 64 tokens of
+// fp16, from shared memory: with Q in shared memory too, one 128 x 64 x 16
+// product reads 6 KB for 32 clocks of work, more than shared memory gives.
+//
+// Warps 0-3 and 4-7: softmax of unit 0 and 1, a query row per thread. Warps
+// 8-11: codes to fp16 tiles (swizzled, sigma c / 128 rounded once: at most
+// |sigma|, so it cannot overflow). Warp 12: issues the products. Warps 13-15:
+// copy codes and scales of one tile each in turn into a ring of raw stages, so
+// that memory latency is hidden by depth, not by registers. O is rescaled only
+// when a row's maximum grows by more than 2^8 over the reference its weights use
+// (the weights stay below 2^15; the final quotient does not see the reference).
+//
+// The query row is scaled by a power of two to [2^13, 2^14) and rounded to
+// fp16. For fp16 outputs (EXACT) queries, keys and weights are split into an
+// fp16 value and its rest; the scores take the three products that matter, the
+// values the two of the weights. What remains is the rounding of the values, half
+// a step of fp16, like the output's own. For bf16 outputs, with steps 8 times as
+// wide, one product each is enough.
+//
+// What bounds it: 128 rows x 64 tokens are 512 clocks of the special function
+// units and, at d = 128, 512 of the tensor cores.
+#pragma once
+
+#include "prefix_mma.cuh"
+
+namespace srftq {
+
+template <int D, int BITS, int G, bool EXACT, bool SHARED>
+struct PrefixPair {
+  static_assert(!(EXACT && SHARED), "fp16 outputs take the split form");
+  static constexpr int TN = 64;
+  static constexpr int CB = D * BITS / 8, NG = D / G, SB = 2 * NG;
+  static constexpr int kPieces = D / 64;
+  static constexpr int kTPiece = TN * 128, kT = kPieces * kTPiece;
+  static constexpr int kKT = kT * (EXACT ? 2 : 1);
+  static constexpr int kSlots = EXACT ? 3 : SHARED ? 3 : 4;         // decoded tiles
+  static constexpr int kSlot = kKT + kT;
+  // a raw stage: rows of K, rows of V, scale rows of K, of V (4 bytes at least)
+  static constexpr int SBS = SB < 4 ? 4 : SB;
+  static constexpr int kRawV = TN * CB, kRawKS = 2 * TN * CB, kRawVS = kRawKS + TN * SBS;
+  static constexpr int kRawStage = kRawVS + TN * SBS;
+  static constexpr int kRaws = BITS == 4 ? 6 : 4;
+  static constexpr int kSlotOff = 0;
+  static constexpr int kRawOff = kSlots * kSlot;
+  static constexpr int kOnOff = kRawOff + kRaws * kRawStage;        // uint32 [raws][2], [16][2]
+  static constexpr int kBarOff = kOnOff + 8 * (kRaws + 16);
+  static constexpr int kBars = 2 * kRaws + 4 * kSlots + 7;
+  static constexpr int kBytes = kBarOff + 8 * kBars + 16;
+  static constexpr int kSmem = kBytes + 1024;                       // slack to start on 1024 bytes
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr int kThreads = 512;
+  static constexpr int kQPieceBytes = kMmaRows * 128;               // a piece of a query tile
+  // tensor memory columns: queries, score tiles, accumulators
+  static constexpr int kQCol = 0, kSCol = 128, kOCol = 256;
+  static constexpr uint32_t kIdescS = f16_idesc<128, TN>();
+  static constexpr uint32_t kIdescO = f16_idesc<128, D>() | (1u << 16);   // B is MN-major
+};
+
+// Arrives on `bar` when this thread's cp.async copies so far have landed (the
+// arrival is one of the barrier's count).
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+template <int D, int BITS, int G, bool EXACT, bool SHARED>
+__global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a) {
+  using L = PrefixPair<D, BITS, G, EXACT, SHARED>;
+  constexpr int TN = L::TN, CB = L::CB, NG = L::NG, NS = L::kSlots, NR = L::kRaws;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_a = smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((0u - raw_a) & 1023u);
+  const uint32_t sm = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t *rfull = bars, *rempty = rfull + NR, *kfull = rempty + NR, *kempty = kfull + NS;
+  uint64_t *vfull = kempty + NS, *vempty = vfull + NS;
+  uint64_t *sfull = vempty + NS, *pfull = sfull + 2, *qfull = pfull + 2, *all_done = qfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(all_done + 2);
+  volatile uint32_t* on_raw = reinterpret_cast<volatile uint32_t*>(smem + L::kOnOff);
+  volatile uint32_t* on_ring = on_raw + 2 * NR;   // by tile, 16 of them
+
+  // this block's head, rows and tokens
+  constexpr int ROWS = SHARED ? 2 * kMmaRows : kMmaRows;
+  const int g = a.q_per_kv, M = a.n_seq * g;
+  const int blocks = (M + ROWS - 1) / ROWS, tiles = (M + kMmaRows - 1) / kMmaRows;
+  const int rt = int(blockIdx.x) % blocks, sh = int(blockIdx.x) / blocks;
+  const int h = sh % a.heads, part_i = sh / a.heads;
+  const int t0 = part_i * a.prefix_per, t1 = min(t0 + a.prefix_per, a.prefix_len);
+  const int n = (t1 - t0 + TN - 1) / TN;                           // tiles of 64 tokens
+  // units with rows: both, or (shared, an odd last tile of rows) the first
+  const int units = SHARED && 2 * rt + 1 >= tiles ? 1 : 2;
+
+  if (tid == 0) {
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(&rfull[i], 33);
+      mbar_init(&rempty[i], 4);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kfull[i], 4);
+      mbar_init(&kempty[i], 1);
+      mbar_init(&vfull[i], 4);
+      mbar_init(&vempty[i], 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&sfull[u], 1);
+      mbar_init(&pfull[u], 4);
+      mbar_init(&qfull[u], 4);
+    }
+    mbar_init(all_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_launch_dependents();
+  grid_dependency_wait();   // the query tiles
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 12) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_or_abort(bar, parity, abort_flag, a.guard);
+        tc_fence_after();
+        return ok;
+      };
+      // S of unit u = Q K^T of tile j
+      auto scores = [&](int u, int j) {
+        const uint32_t dt = tmem + L::kSCol + 64 * u;
+        const uint32_t q = tmem + L::kQCol + (SHARED ? D / 2 * u : 0);
+        const uint32_t kb = sm + L::kSlotOff + (j % NS) * L::kSlot;
+#pragma unroll
+        for (int pc = 0; pc < L::kPieces; ++pc)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t kd = sw128_desc(kb + pc * L::kTPiece + 32u * ks);
+            tc_mma_f16_ts(dt, q + 32 * pc + 8 * ks, kd, L::kIdescS, (pc | ks) != 0 ? 1u : 0u);
+            if constexpr (EXACT) {
+              tc_mma_f16_ts(dt, q + D / 2 + 32 * pc + 8 * ks, kd, L::kIdescS, 1u);
+              tc_mma_f16_ts(dt, q + 32 * pc + 8 * ks,
+                            sw128_desc(kb + L::kT + pc * L::kTPiece + 32u * ks), L::kIdescS, 1u);
+            }
+          }
+        tc_commit(&sfull[u]);
+      };
+      // O of unit u += P V of tile j, its m-th
+      auto values = [&](int u, int j, int m) {
+        const uint32_t vb = sm + L::kSlotOff + (j % NS) * L::kSlot + L::kKT;
+        const uint32_t pt = tmem + L::kSCol + 64 * u, ot = tmem + L::kOCol + 128 * u;
+#pragma unroll
+        for (int ks = 0; ks < TN / 16; ++ks) {
+          const uint64_t bd = sw128_mn_desc(vb + 2048u * ks, L::kTPiece);
+          tc_mma_f16_ts(ot, pt + 8 * ks, bd, L::kIdescO, (m | ks) != 0 ? 1u : 0u);
+          if constexpr (EXACT) tc_mma_f16_ts(ot, pt + TN / 2 + 8 * ks, bd, L::kIdescO, 1u);
+        }
+      };
+      bool ok = wait(&qfull[0], 0) && (SHARED && units == 2 ? wait(&qfull[1], 0) : true);
+      if constexpr (SHARED) {
+        for (int j = 0; j <= n && ok; ++j) {
+          if (j < n) ok = wait(&kfull[j % NS], (j / NS) & 1);
+          if (ok && j > 0) ok = wait(&vfull[(j - 1) % NS], ((j - 1) / NS) & 1);
+          for (int u = 0; u < units && ok; ++u) {
+            if (j > 0) {
+              ok = wait(&pfull[u], (j - 1) & 1);
+              if (!ok) break;
+              values(u, j - 1, j - 1);
+            }
+            if (j < n) scores(u, j);
+          }
+          if (!ok) break;
+          if (j < n) tc_commit(&kempty[j % NS]);
+          if (j > 0) tc_commit(&vempty[(j - 1) % NS]);
+        }
+      } else {
+        for (int j = 0; j < n + 2 && ok; ++j) {
+          const int u = j & 1, m = j >> 1;
+          if (m > 0 && j - 2 < n) {
+            ok = wait(&vfull[(j - 2) % NS], ((j - 2) / NS) & 1) && wait(&pfull[u], (m - 1) & 1);
+            if (!ok) break;
+            values(u, j - 2, m - 1);
+            tc_commit(&vempty[(j - 2) % NS]);
+          }
+          if (j < n) {
+            ok = wait(&kfull[j % NS], (j / NS) & 1);
+            if (!ok) break;
+            scores(u, j);
+            tc_commit(&kempty[j % NS]);
+          }
+        }
+      }
+      tc_commit(all_done);   // every product is done before tensor memory is freed
+      (void)mbar_wait_bounded(all_done, 0);
+    }
+  } else if (warp > 12) {
+    // ---------------- loaders: tile j by warp 13 + j % 3 ----------------
+    constexpr int PPT = CB / 16, NK = TN * PPT / 32;   // pieces of a row, of a lane
+    int32_t page[2];
+    auto look_up = [&](int j) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int t = t0 + j * TN + lane + 32 * k;
+        page[k] = j < n && t < t1 ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t))) : -1;
+      }
+    };
+    look_up(warp - 13);
+    for (int j = warp - 13; j < n; j += 3) {
+      const int st = j % NR;
+      int32_t row[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t t = uint32_t(t0 + j * TN + lane + 32 * k);
+        row[k] = uint32_t(page[k]) < uint32_t(a.map.n_pages)
+                     ? int32_t(uint32_t(page[k]) * a.map.page.d + (t - a.map.page.div(t) * a.map.page.d))
+                     : -1;
+      }
+      look_up(j + 3);
+      if (j >= NR && !__all_sync(0xffffffffu, wait_or_abort(&rempty[st], ((j / NR) & 1) ^ 1,
+                                                            abort_flag, a.guard)))
+        break;
+      const uint32_t rb = sm + L::kRawOff + st * L::kRawStage;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const int p = lane + 32 * i, tok = p / PPT, pc = p % PPT;
+        const int32_t r = __shfl_sync(0xffffffffu, row[(32 * i) / PPT / 32], tok & 31);
+        const int64_t at = (int64_t(r < 0 ? 0 : r) * a.heads + h) * CB + pc * 16;
+        copy16(rb + p * 16, a.k_codes + at, r >= 0);
+        copy16(rb + L::kRawV + p * 16, a.v_codes + at, r >= 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t vec = int64_t(row[k] < 0 ? 0 : row[k]) * a.heads + h;
+        const uint16_t *ks = a.k_scales + vec * NG, *vs = a.v_scales + vec * NG;
+        const uint32_t dk = rb + L::kRawKS + (lane + 32 * k) * L::SBS, dv = dk + TN * L::SBS;
+        if constexpr (L::SB >= 16) {
+          copy16(dk, ks, row[k] >= 0);
+          copy16(dv, vs, row[k] >= 0);
+        } else if constexpr (L::SB >= 4) {
+          copy_small<L::SB>(dk, ks, row[k] >= 0);
+          copy_small<L::SB>(dv, vs, row[k] >= 0);
+        } else {   // one scale: 2 bytes, below the smallest asynchronous copy
+          const uint32_t x = row[k] >= 0 ? __ldg(ks) : 0u, y = row[k] >= 0 ? __ldg(vs) : 0u;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dk), "r"(x) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dv), "r"(y) : "memory");
+        }
+      }
+      const uint32_t on0 = __ballot_sync(0xffffffffu, row[0] >= 0);
+      const uint32_t on1 = __ballot_sync(0xffffffffu, row[1] >= 0);
+      copies_arrive(&rfull[st]);
+      __syncwarp();
+      if (lane == 0) {
+        on_raw[2 * st] = on0;
+        on_raw[2 * st + 1] = on1;
+        __threadfence_block();
+        mbar_arrive(&rfull[st]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= 8) {
+    // ---------------- codes to fp16 tiles ----------------
+    // Neighbouring threads take the 16-byte pieces of one row.
+    constexpr int PPT = CB / 16, RPP = 128 / PPT;        // pieces of a row, rows per pass
+    constexpr int NK = TN / RPP, CC = 128 / BITS;        // pieces of a thread, coordinates of one
+    constexpr bool TWO = CC > G;                         // two scales to a piece
+    const int dt = tid - 256, pc = dt % PPT, tr = dt / PPT;
+    uint4 w[NK];
+    uint32_t s[NK];
+    auto fetch = [&](uint32_t codes, uint32_t scales) {
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        w[k] = lds128(codes + (dt + 128 * k) * 16);
+        const uint32_t sa = scales + (tr + k * RPP) * L::SBS + pc * CC / G * 2;
+        if constexpr (TWO) {
+          s[k] = lds32(sa);
+        } else {
+          uint16_t x;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(sa));
+          s[k] = x;
+        }
+      }
+    };
+    for (int j = 0; j < n; ++j) {
+      const int st = j % NR, sl = j % NS;
+      if (!__all_sync(0xffffffffu,
+                      wait_or_abort(&rfull[st], (j / NR) & 1, abort_flag, a.guard)))
+        break;
+      const uint32_t rb = sm + L::kRawOff + st * L::kRawStage;
+      const uint32_t tb = sm + L::kSlotOff + sl * L::kSlot;
+      fetch(rb, rb + L::kRawKS);
+      // an entry of the ring is written again 16 tiles on, long after the
+      // softmax of this tile: at most the slots' tiles lie between
+      if (tid == 256) {
+        on_ring[2 * (j & 15)] = on_raw[2 * st];
+        on_ring[2 * (j & 15) + 1] = on_raw[2 * st + 1];
+        __threadfence_block();
+      }
+      if (j >= NS && !__all_sync(0xffffffffu, wait_or_abort(&kempty[sl], ((j / NS) & 1) ^ 1,
+                                                            abort_flag, a.guard)))
+        break;
+      decode_pieces<D, BITS, G, TN, EXACT, NK>(tb, L::kT, pc, tr, w, s);
+      fetch(rb + L::kRawV, rb + L::kRawVS);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&kfull[sl]);
+        mbar_arrive(&rempty[st]);
+      }
+      if (j >= NS && !__all_sync(0xffffffffu, wait_or_abort(&vempty[sl], ((j / NS) & 1) ^ 1,
+                                                            abort_flag, a.guard)))
+        break;
+      decode_pieces<D, BITS, G, TN, false, NK>(tb + L::kKT, 0, pc, tr, w, s);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&vfull[sl]);
+    }
+  } else {
+    // ---------------- softmax: a query row per thread ----------------
+    const int u = warp >> 2, r = tid & 127;
+    const int tile_i = SHARED ? 2 * rt + u : rt;         // 128-row tile of the head
+    const int r0 = tile_i * kMmaRows;
+    const int n_mine = SHARED ? n : (n + 1 - u) / 2;     // tiles of this unit
+    if (u < units) {
+      const uint32_t tl = tmem + (uint32_t(warp & 3) << 21);
+      const uint32_t tS = tl + L::kSCol + 64 * u, tO = tl + L::kOCol + 128 * u;
+      const int64_t tile = int64_t(h) * tiles + tile_i;
+      bool ok = true;
+      if (SHARED || u == 0) {   // the rows' queries to tensor memory
+        const uint8_t* img = a.q_image + tile * (256 * D * (EXACT ? 2 : 1)) + r * 128;
+#pragma unroll 1
+        for (int i = 0; i < L::kPieces * (EXACT ? 2 : 1); ++i) {
+          uint32_t x[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(img + i * L::kQPieceBytes + ((c ^ (r & 7)) << 4));
+            x[4 * c] = v.x;
+            x[4 * c + 1] = v.y;
+            x[4 * c + 2] = v.z;
+            x[4 * c + 3] = v.w;
+          }
+          tmem_st32(tl + L::kQCol + (SHARED ? D / 2 * u : 0) + 32 * i, x);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[u]);
+      }
+      const int rr = min(r0 + r, M - 1);
+      const int lim = a.len(rr / g);
+      const float f = a.q_factor[tile * kMmaRows + r];
+      float ref = -INFINITY, l = 0.0f;       // the reference of the weights, their sum
+      for (int m = 0; m < n_mine; ++m) {
+        const int j = SHARED ? m : 2 * m + u;
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[u], m & 1, abort_flag, a.guard))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[2][32];
+        tmem_ld32(tS, s[0]);
+        tmem_ld32(tS + 32, s[1]);
+        const int tk = t0 + j * TN;
+        const uint32_t on[2] = {on_ring[2 * (j & 15)], on_ring[2 * (j & 15) + 1]};
+        tmem_wait_ld(s[0], s[1]);
+        if (!__all_sync(0xffffffffu, (on[0] & on[1]) == 0xffffffffu && tk + TN <= lim)) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((on[k] >> i) & 1u) || tk + 32 * k + i >= lim) s[k][i] = 0xff800000u;
+        }
+        float mx = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            mx = max3(mx, __uint_as_float(s[k][i]), __uint_as_float(s[k][i + 1]));
+            mx1 = max3(mx1, __uint_as_float(s[k][i + 2]), __uint_as_float(s[k][i + 3]));
+          }
+        mx = fmaxf(mx, mx1) * f;             // f > 0
+        const bool grow = mx > ref + 8.0f || (ref == -INFINITY && mx > -INFINITY);
+        const float nref = grow ? mx : ref;
+        const float cc = !grow ? 1.0f : ref == -INFINITY ? 0.0f : ex2(ref - nref);
+        l *= cc;
+        ref = nref;
+        // P = 2^7 e^{x - ref} (0 while the row has seen no token)
+        const float b = 7.0f - (ref == -INFINITY ? 0.0f : ref);
+        float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
+        uint32_t ph[32];
+        uint32_t pl[EXACT ? 32 : 1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(s[k][i]), __uint_as_float(s[k][i + 1])),
+                make_float2(f, f), make_float2(b, b));
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+            if (i & 2) sum1 = __fadd2_rn(sum1, p);
+            else sum = __fadd2_rn(sum, p);
+            const uint32_t hh = pack_half2(p.x, p.y);
+            ph[16 * k + i / 2] = hh;
+            if constexpr (EXACT) pl[16 * k + i / 2] = half2_rest(p.x, p.y, hh);
+          }
+        l += (sum.x + sum.y) + (sum1.x + sum1.y);
+        tmem_st32(tS, ph);
+        if constexpr (EXACT) tmem_st32(tS + 32, pl);
+        // O follows the reference; these scores came after the values of every
+        // earlier tile of the unit, so it is complete up to there
+        if (m > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+          for (int k = 0; k < D; k += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + k, o);
+            tmem_wait_ld1(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * cc);
+            tmem_st32(tO + k, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[u]);
+      }
+      if (ok && __all_sync(0xffffffffu, wait_or_abort(all_done, 0, abort_flag, a.guard))) {
+        tc_fence_after();
+        const int64_t part = (int64_t(SHARED ? part_i : 2 * part_i + u) * a.heads + h) * M + r0 + r;
+        const bool live = r0 + r < M;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          uint32_t o[32];
+          if (n_mine > 0) {
+            tmem_ld32(tO + k, o);
+            tmem_wait_ld1(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (live) {
+            float y[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)   // 128 / 2^7 = 1
+              y[(i & ~7) + decoded_coord<BITS>(i & 7)] =
+                  __uint_as_float(o[i]) * (decoded_times16<BITS>(i & 7) ? 0.0625f : 1.0f);
+            float4* dst = reinterpret_cast<float4*>(a.pre_acc + part * D + k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
+        }
+        if (live) a.pre_ml[part] = make_float2(ref, l * 0x1p-7f);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace srftq
