@@ -145,13 +145,15 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
     else prefix_prepare_kernel<kSRHT, D><<<g1, 256, 0, c.stream>>>(a);
     rc = launch_prefix_tiles<D>(a, c.bits, c.group, c.stream);
     if (rc != SRFTQ_OK) return;
-    // few query heads: more warps each, since then a block's own time counts
-    static_for<0, 2>([&](auto w_) {
-      constexpr int NW = decltype(w_)::value ? 16 : 4;
-      if ((queries <= 2 * sms) != (NW == 16)) return;
+    // few query heads: more warps each, since then a block's own time counts;
+    // very many: a warp each, for the blocks' barriers cost more than they save
+    static_for<0, 3>([&](auto w_) {
+      constexpr int NW = decltype(w_)::value == 0 ? 1 : decltype(w_)::value == 1 ? 4 : 16;
+      if ((queries <= 2 * sms ? 16 : queries <= 16 * sms ? 4 : 1) != NW) return;
+      const int grid = int(NW == 1 ? (queries + 3) / 4 : queries), threads = NW == 1 ? 128 : 32 * NW;
       rc = c.rotation == kSRFT
-               ? launch_after<prefix_merge_kernel<kSRFT, D, NW>>(int(queries), 32 * NW, 0, c.stream, a)
-               : launch_after<prefix_merge_kernel<kSRHT, D, NW>>(int(queries), 32 * NW, 0, c.stream, a);
+               ? launch_after<prefix_merge_kernel<kSRFT, D, NW>>(grid, threads, 0, c.stream, a)
+               : launch_after<prefix_merge_kernel<kSRHT, D, NW>>(grid, threads, 0, c.stream, a);
     });
     if (rc != SRFTQ_OK) return;
     rc = finish_launch();

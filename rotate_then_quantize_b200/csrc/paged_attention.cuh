@@ -804,18 +804,19 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
   }
 }
 
-// A block per query head: the parts' (m, l) by all threads, then their
-// weighted sums a warp per part in turn, added over the warps in order, and
-// the rotation by the first warp.
+// NW warps per query head, four heads to a block of the one-warp form. The parts'
+// (m, l) by all lanes, then their weighted sums, a warp a part in turn, added over
+// the warps in order; the rotation by the first warp.
 template <int ROT, int D, int NW>
-__global__ void __launch_bounds__(NW * 32) prefix_merge_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32) prefix_merge_kernel(const PrefixArgs a) {
   constexpr int E = D / 64;
-  grid_dependency_wait();
   __shared__ float acc_sh[NW][D];
   __shared__ float2 ml_sh[NW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : int(threadIdx.x >> 5);
   const int g = a.q_per_kv, hq = a.heads * g;
-  const int64_t v = blockIdx.x;
+  const int64_t v = NW == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+  if (NW == 1 && v >= int64_t(a.n_seq) * hq) return;
   const int b = int(v / hq), h = int(v % hq) / g, j = int(v % hq) % g;
   const int64_t M = int64_t(a.n_seq) * g;
   const int n_pre = a.prefix_len > 0 && a.len(b) > 0 ? a.prefix_splits : 0;
@@ -828,19 +829,26 @@ __global__ void __launch_bounds__(NW * 32) prefix_merge_kernel(const PrefixArgs 
   auto ml_of = [&](int i) { return (i < n_pre ? a.pre_ml : a.own_ml)[row_of(i)]; };
   // a part without tokens has l = 0 (a NaN goes on)
   float m = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += NW * 32) m = fmaxf(m, ml_of(i).x);
+  for (int i = NW == 1 ? lane : int(threadIdx.x); i < n; i += NW * 32) m = fmaxf(m, ml_of(i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) ml_sh[warp].x = m;
-  __syncthreads();
+  if constexpr (NW > 1) {
+    if (lane == 0) ml_sh[warp].x = m;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) m = fmaxf(m, ml_sh[w].x);
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, ml_sh[w].x);
+  }
   const float ref = m == -INFINITY ? 0.0f : m;
 
   float l = 0.0f;
   float2 acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = make_float2(0.0f, 0.0f);
+  // the one-warp form loads the pairs that its lanes rotate, the others pass
+  // them through shared memory
+  int at[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) at[e] = NW == 1 ? warp_pair<ROT, D>(lane, e) : lane + 32 * e;
 #pragma unroll 4
   for (int i = warp; i < n; i += NW) {
     const int64_t r = row_of(i);
@@ -848,7 +856,7 @@ __global__ void __launch_bounds__(NW * 32) prefix_merge_kernel(const PrefixArgs 
     const float2* src = reinterpret_cast<const float2*>((i < n_pre ? a.pre_acc : a.own_acc) + r * D);
     float2 x[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = src[lane + 32 * e];
+    for (int e = 0; e < E; ++e) x[e] = src[at[e]];
     if (ml.y > 0.0f || ml.y != ml.y) {
       const float c = exp2f(ml.x - ref);
       l = fmaf(ml.y, c, l);
@@ -857,27 +865,31 @@ __global__ void __launch_bounds__(NW * 32) prefix_merge_kernel(const PrefixArgs 
         acc[e] = make_float2(fmaf(x[e].x, c, acc[e].x), fmaf(x[e].y, c, acc[e].y));
     }
   }
-  if (lane == 0) ml_sh[warp].y = l;
+  if constexpr (NW > 1) {
+    if (lane == 0) ml_sh[warp].y = l;
 #pragma unroll
-  for (int e = 0; e < E; ++e) reinterpret_cast<float2*>(acc_sh[warp])[lane + 32 * e] = acc[e];
-  __syncthreads();
-  if (warp > 0) return;
-  l = 0.0f;
+    for (int e = 0; e < E; ++e) reinterpret_cast<float2*>(acc_sh[warp])[lane + 32 * e] = acc[e];
+    __syncthreads();
+    if (warp > 0) return;
+    l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) l += ml_sh[w].y;
+    for (int w = 0; w < NW; ++w) l += ml_sh[w].y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      acc[e] = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float2 x = reinterpret_cast<const float2*>(acc_sh[w])[warp_pair<ROT, D>(lane, e)];
+        acc[e] = make_float2(acc[e].x + x.x, acc[e].y + x.y);
+      }
+    }
+  }
   const float inv = l > 0.0f ? 1.0f / l : l;   // no token: 0 (a NaN stays)
   const float2* lam = reinterpret_cast<const float2*>(a.v_lambda + int64_t(h) * D);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int k = warp_pair<ROT, D>(lane, e);
-    const float2 f = lam[k];
-    float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float2 x = reinterpret_cast<const float2*>(acc_sh[w])[k];
-      s = make_float2(s.x + x.x, s.y + x.y);
-    }
-    acc[e] = make_float2(s.x * inv * f.x, s.y * inv * f.y);
+    const float2 f = lam[warp_pair<ROT, D>(lane, e)];
+    acc[e] = make_float2(acc[e].x * inv * f.x, acc[e].y * inv * f.y);
   }
   warp_rotate_inverse<ROT, D>(acc, lane);
   const int8_t* sg = a.v_signs + int64_t(h) * D + 2 * E * lane;

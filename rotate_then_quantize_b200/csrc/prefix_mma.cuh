@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
       const int tk = t0 + i * TN;
       // bit j of on[k]: token 32 k + j of the step is there
       uint32_t on[TN / 32];
-      bool all = tk + TN <= lim;
+      const bool past = lim <= tk;   // the row ends before: its weights are 0 below
+      bool all = past || tk + TN <= lim;
 #pragma unroll
       for (int k = 0; k < TN / 32; ++k) {
         on[k] = __ballot_sync(0xffffffffu, on_sh[(i & 3) * TN + 32 * k + lane] != 0);
@@ -383,15 +384,14 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
           mx = max3(mx, __uint_as_float(s[k][j]), __uint_as_float(s[k][j + 1]));
           mx1 = max3(mx1, __uint_as_float(s[k][j + 2]), __uint_as_float(s[k][j + 3]));
         }
-      mx = fmaxf(mx, mx1);
-      mx *= f;                               // f > 0
+      mx = past ? -INFINITY : fmaxf(mx, mx1) * f;   // f > 0
       const bool grow = mx > ref + 8.0f || (ref == -INFINITY && mx > -INFINITY);
       const float nref = grow ? mx : ref;
       const float cc = !grow ? 1.0f : ref == -INFINITY ? 0.0f : ex2(ref - nref);
       l *= cc;
       ref = nref;
       // P = 2^7 e^{x - ref} (0 while the row has seen no token)
-      const float b = 7.0f - (ref == -INFINITY ? 0.0f : ref);
+      const float b = past ? -INFINITY : 7.0f - (ref == -INFINITY ? 0.0f : ref);
       float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
       uint32_t ph[32];
       uint32_t pl[EXACT ? 32 : 1];

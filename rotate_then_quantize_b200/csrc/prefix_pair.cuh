@@ -1,26 +1,23 @@
 // Parts of the shared prefix on the 5th-generation tensor cores (tcgen05) for
 // d = 64 and 128: two units of 128 query rows on each SM.
 //
-// A unit is 128 query rows with a score tile S, weights P over it, and an
-// accumulator O, all in tensor memory, the rows' queries too:
+// A unit is 128 query rows with two score tiles S, the weights P written over
+// them, and an accumulator O, all in tensor memory:
 //   S[row][token]  = Q (sigma c / 128)^T      TN = 64 tokens at a time;
 //   P[row][token]  = 2^7 e^{x - ref}, fp16, written over S;
 //   O[row][coord] += P (sigma c / 128).
-// While one unit's four warps take exponentials the tensor cores form the other
-// unit's products, so the special function units always have work. Two forms:
+// The scores of a unit's next tile are formed while its four warps take the
+// exponentials of this one. Two forms:
 //   shared   the units are 256 different rows over the same tokens: a token's
 //            codes are decoded once for both (bf16 outputs, more than 128 rows);
 //   split    the units are the same rows over alternate tiles, two parts of the
 //            softmax (up to 128 rows, and fp16 outputs).
-// The left operands come from tensor memory and the right ones, 64 tokens of
-// fp16, from shared memory: with Q in shared memory too, one 128 x 64 x 16
-// product reads 6 KB for 32 clocks of work, more than shared memory gives.
 //
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, a query row per thread. Warps
 // 8-11: codes to fp16 tiles (swizzled, sigma c / 128 rounded once: at most
-// |sigma|, so it cannot overflow). Warp 12: issues the products. Warps 13-15:
-// copy codes and scales of one tile each in turn into a ring of raw stages, so
-// that memory latency is hidden by depth, not by registers. O is rescaled only
+// |sigma|, so it cannot overflow). Warps 12 and 13: issue the units' products.
+// Warps 14 and 15: copy codes and scales of one tile each in turn into a ring of
+// raw stages, so that memory latency is hidden by depth, not by registers. O is rescaled only
 // when a row's maximum grows by more than 2^8 over the reference its weights use
 // (the weights stay below 2^15; the final quotient does not see the reference).
 //
@@ -47,25 +44,27 @@ struct PrefixPair {
   static constexpr int kPieces = D / 64;
   static constexpr int kTPiece = TN * 128, kT = kPieces * kTPiece;
   static constexpr int kKT = kT * (EXACT ? 2 : 1);
-  static constexpr int kSlots = EXACT ? 3 : SHARED ? 3 : 4;         // decoded tiles
-  static constexpr int kSlot = kKT + kT;
+  static constexpr int kQTile = kPieces * kMmaRows * 128 * (EXACT ? 2 : 1);
+  static constexpr int kQ = kQTile * (SHARED ? 2 : 1);
+  static constexpr int kSlots = EXACT ? 2 : BITS == 8 ? (SHARED ? 2 : 3) : SHARED ? 3 : 4;
+  static constexpr int kSlot = kKT + kT;                            // a decoded tile
   // a raw stage: rows of K, rows of V, scale rows of K, of V (4 bytes at least)
   static constexpr int SBS = SB < 4 ? 4 : SB;
   static constexpr int kRawV = TN * CB, kRawKS = 2 * TN * CB, kRawVS = kRawKS + TN * SBS;
   static constexpr int kRawStage = kRawVS + TN * SBS;
-  static constexpr int kRaws = BITS == 4 ? 6 : 4;
-  static constexpr int kSlotOff = 0;
-  static constexpr int kRawOff = kSlots * kSlot;
+  static constexpr int kRaws = BITS == 4 ? 6 : EXACT ? 3 : 4;
+  static constexpr int kSlotOff = kQ;
+  static constexpr int kRawOff = kSlotOff + kSlots * kSlot;
   static constexpr int kOnOff = kRawOff + kRaws * kRawStage;        // uint32 [raws][2], [16][2]
   static constexpr int kBarOff = kOnOff + 8 * (kRaws + 16);
-  static constexpr int kBars = 2 * kRaws + 4 * kSlots + 7;
+  static constexpr int kBars = 2 * kRaws + 4 * kSlots + 13;
   static constexpr int kBytes = kBarOff + 8 * kBars + 16;
   static constexpr int kSmem = kBytes + 1024;                       // slack to start on 1024 bytes
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static constexpr int kThreads = 512;
-  static constexpr int kQPieceBytes = kMmaRows * 128;               // a piece of a query tile
-  // tensor memory columns: queries, score tiles, accumulators
-  static constexpr int kQCol = 0, kSCol = 128, kOCol = 256;
+  static constexpr int kQPiece = kMmaRows * 128;                    // a piece of a query tile
+  // tensor memory columns: score tiles (two of each unit), accumulators
+  static constexpr int kSCol = 0, kOCol = 256;
   static constexpr uint32_t kIdescS = f16_idesc<128, TN>();
   static constexpr uint32_t kIdescO = f16_idesc<128, D>() | (1u << 16);   // B is MN-major
 };
@@ -85,11 +84,14 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
   const uint32_t raw_a = smem_addr(smem_raw);
   uint8_t* smem = smem_raw + ((0u - raw_a) & 1023u);
   const uint32_t sm = smem_addr(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in the warp's lanes
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t *rfull = bars, *rempty = rfull + NR, *kfull = rempty + NR, *kempty = kfull + NS;
   uint64_t *vfull = kempty + NS, *vempty = vfull + NS;
-  uint64_t *sfull = vempty + NS, *pfull = sfull + 2, *qfull = pfull + 2, *all_done = qfull + 2;
+  // scores and weights by unit and tile (2 u + buffer), values by unit
+  uint64_t *sfull = vempty + NS, *pfull = sfull + 4, *odone = pfull + 4, *qfull = odone + 2;
+  uint64_t* all_done = qfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(all_done + 2);
   volatile uint32_t* on_raw = reinterpret_cast<volatile uint32_t*>(smem + L::kOnOff);
@@ -113,16 +115,17 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kfull[i], 4);
-      mbar_init(&kempty[i], 1);
+      mbar_init(&kempty[i], SHARED ? units : 1);   // an arrival of each unit that reads it
       mbar_init(&vfull[i], 4);
-      mbar_init(&vempty[i], 1);
+      mbar_init(&vempty[i], SHARED ? units : 1);
     }
-    for (int u = 0; u < 2; ++u) {
-      mbar_init(&sfull[u], 1);
-      mbar_init(&pfull[u], 4);
-      mbar_init(&qfull[u], 4);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
     }
-    mbar_init(all_done, 1);
+    for (int u = 0; u < 2; ++u) mbar_init(&odone[u], 1);
+    for (int u = 0; u < 2; ++u) mbar_init(&qfull[u], 1);
+    mbar_init(all_done, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -137,83 +140,87 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
   grid_dependency_wait();   // the query tiles
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 12) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+  if (warp == 12 || warp == 13) {
+    // ---------------- MMA issuers, one for each unit ----------------
+    // The whole warp runs this and every operand is the same in its lanes, so
+    // addresses and descriptors stay in uniform registers; one elected lane
+    // issues. (From a branch of one lane each product waits for its operands to
+    // be moved there: 131072 int8 tokens for 128 rows took 239 instead of 157 us.)
+    {
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = wait_or_abort(bar, parity, abort_flag, a.guard);
+        const bool ok =
+            __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.guard));
         tc_fence_after();
         return ok;
       };
-      // S of unit u = Q K^T of tile j
-      auto scores = [&](int u, int j) {
-        const uint32_t dt = tmem + L::kSCol + 64 * u;
-        const uint32_t q = tmem + L::kQCol + (SHARED ? D / 2 * u : 0);
-        const uint32_t kb = sm + L::kSlotOff + (j % NS) * L::kSlot;
+      // S of unit u = Q K^T of the tile in slot sl, the unit's m-th
+      const uint64_t q0 = sw128_desc(sm);
+      auto scores = [&](int u, int sl, int m) {
+        const uint32_t dt = tm + L::kSCol + 128 * u + 64 * (m & 1);
+        const uint64_t qd = q0 + (SHARED ? u * (L::kQTile >> 4) : 0);
+        const uint64_t k0 = sw128_desc(sm + L::kSlotOff + sl * L::kSlot);
 #pragma unroll
         for (int pc = 0; pc < L::kPieces; ++pc)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t kd = sw128_desc(kb + pc * L::kTPiece + 32u * ks);
-            tc_mma_f16_ts(dt, q + 32 * pc + 8 * ks, kd, L::kIdescS, (pc | ks) != 0 ? 1u : 0u);
+            const uint64_t qk = qd + ((pc * L::kQPiece + 32 * ks) >> 4);
+            const uint64_t kd = k0 + ((pc * L::kTPiece + 32 * ks) >> 4);
+            tc_mma_f16_elect(dt, qk, kd, L::kIdescS, (pc | ks) != 0 ? 1u : 0u);
             if constexpr (EXACT) {
-              tc_mma_f16_ts(dt, q + D / 2 + 32 * pc + 8 * ks, kd, L::kIdescS, 1u);
-              tc_mma_f16_ts(dt, q + 32 * pc + 8 * ks,
-                            sw128_desc(kb + L::kT + pc * L::kTPiece + 32u * ks), L::kIdescS, 1u);
+              tc_mma_f16_elect(dt, qk + (L::kPieces * L::kQPiece >> 4), kd, L::kIdescS, 1u);
+              tc_mma_f16_elect(dt, qk, kd + (L::kT >> 4), L::kIdescS, 1u);
             }
           }
-        tc_commit(&sfull[u]);
+        tc_commit_elect(&sfull[2 * u + (m & 1)]);
       };
-      // O of unit u += P V of tile j, its m-th
-      auto values = [&](int u, int j, int m) {
-        const uint32_t vb = sm + L::kSlotOff + (j % NS) * L::kSlot + L::kKT;
-        const uint32_t pt = tmem + L::kSCol + 64 * u, ot = tmem + L::kOCol + 128 * u;
+      // O of unit u += P V of the tile in slot sl, the unit's m-th
+      auto values = [&](int u, int sl, int m) {
+        const uint32_t pt = tm + L::kSCol + 128 * u + 64 * (m & 1), ot = tm + L::kOCol + 128 * u;
+        const uint64_t v0 =
+            sw128_mn_desc(sm + L::kSlotOff + sl * L::kSlot + L::kKT, L::kTPiece);
 #pragma unroll
         for (int ks = 0; ks < TN / 16; ++ks) {
-          const uint64_t bd = sw128_mn_desc(vb + 2048u * ks, L::kTPiece);
-          tc_mma_f16_ts(ot, pt + 8 * ks, bd, L::kIdescO, (m | ks) != 0 ? 1u : 0u);
-          if constexpr (EXACT) tc_mma_f16_ts(ot, pt + TN / 2 + 8 * ks, bd, L::kIdescO, 1u);
+          const uint64_t bd = v0 + ((2048 * ks) >> 4);
+          tc_mma_f16_ts_elect(ot, pt + 8 * ks, bd, L::kIdescO, (m | ks) != 0 ? 1u : 0u);
+          if constexpr (EXACT)
+            tc_mma_f16_ts_elect(ot, pt + TN / 2 + 8 * ks, bd, L::kIdescO, 1u);
         }
+        tc_commit_elect(&odone[u]);
       };
-      bool ok = wait(&qfull[0], 0) && (SHARED && units == 2 ? wait(&qfull[1], 0) : true);
-      if constexpr (SHARED) {
-        for (int j = 0; j <= n && ok; ++j) {
-          if (j < n) ok = wait(&kfull[j % NS], (j / NS) & 1);
-          if (ok && j > 0) ok = wait(&vfull[(j - 1) % NS], ((j - 1) / NS) & 1);
-          for (int u = 0; u < units && ok; ++u) {
-            if (j > 0) {
-              ok = wait(&pfull[u], (j - 1) & 1);
-              if (!ok) break;
-              values(u, j - 1, j - 1);
-            }
-            if (j < n) scores(u, j);
-          }
+      const int u = warp - 12;
+      const int n_mine = u < units ? (SHARED ? n : (n + 1 - u) / 2) : 0;
+      uint64_t* my_q = &qfull[SHARED ? u : 0];
+      if (lane == 0 && (SHARED ? u < units : u == 0)) {
+        const int64_t tile = int64_t(h) * tiles + (SHARED ? 2 * rt + u : rt);
+        mbar_arrive_expect_tx(my_q, L::kQTile);
+        bulk_load(smem + (SHARED ? u * L::kQTile : 0), a.q_image + tile * L::kQTile, L::kQTile, my_q);
+      }
+      __syncwarp();
+      bool ok = n_mine == 0 || wait(my_q, 0);
+      // the scores run a tile ahead of the values
+      for (int m = 0; m <= n_mine && ok; ++m) {
+        if (m < n_mine) {
+          const int j = SHARED ? m : 2 * m + u, sl = j % NS;
+          ok = wait(&kfull[sl], (j / NS) & 1);
           if (!ok) break;
-          if (j < n) tc_commit(&kempty[j % NS]);
-          if (j > 0) tc_commit(&vempty[(j - 1) % NS]);
+          scores(u, sl, m);
+          tc_commit_elect(&kempty[sl]);
         }
-      } else {
-        for (int j = 0; j < n + 2 && ok; ++j) {
-          const int u = j & 1, m = j >> 1;
-          if (m > 0 && j - 2 < n) {
-            ok = wait(&vfull[(j - 2) % NS], ((j - 2) / NS) & 1) && wait(&pfull[u], (m - 1) & 1);
-            if (!ok) break;
-            values(u, j - 2, m - 1);
-            tc_commit(&vempty[(j - 2) % NS]);
-          }
-          if (j < n) {
-            ok = wait(&kfull[j % NS], (j / NS) & 1);
-            if (!ok) break;
-            scores(u, j);
-            tc_commit(&kempty[j % NS]);
-          }
+        if (m > 0) {
+          const int i = m - 1, j = SHARED ? i : 2 * i + u, sl = j % NS;
+          ok = wait(&vfull[sl], (j / NS) & 1) && wait(&pfull[2 * u + (i & 1)], (i >> 1) & 1);
+          if (!ok) break;
+          values(u, sl, i);
+          tc_commit_elect(&vempty[sl]);
         }
       }
-      tc_commit(all_done);   // every product is done before tensor memory is freed
+      tc_commit_elect(all_done);   // every product is done before tensor memory is freed
       (void)mbar_wait_bounded(all_done, 0);
+      __syncwarp();
     }
-  } else if (warp > 12) {
-    // ---------------- loaders: tile j by warp 13 + j % 3 ----------------
+  } else if (warp > 13) {
+    // ---------------- loaders: tile j by warp 14 + j % 2 ----------------
     constexpr int PPT = CB / 16, NK = TN * PPT / 32;   // pieces of a row, of a lane
     int32_t page[2];
     auto look_up = [&](int j) {
@@ -223,8 +230,8 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         page[k] = j < n && t < t1 ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t))) : -1;
       }
     };
-    look_up(warp - 13);
-    for (int j = warp - 13; j < n; j += 3) {
+    look_up(warp - 14);
+    for (int j = warp - 14; j < n; j += 2) {
       const int st = j % NR;
       int32_t row[2];
 #pragma unroll
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
                      ? int32_t(uint32_t(page[k]) * a.map.page.d + (t - a.map.page.div(t) * a.map.page.d))
                      : -1;
       }
-      look_up(j + 3);
+      look_up(j + 2);
       if (j >= NR && !__all_sync(0xffffffffu, wait_or_abort(&rempty[st], ((j / NR) & 1) ^ 1,
                                                             abort_flag, a.guard)))
         break;
@@ -341,37 +348,18 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
     const int n_mine = SHARED ? n : (n + 1 - u) / 2;     // tiles of this unit
     if (u < units) {
       const uint32_t tl = tmem + (uint32_t(warp & 3) << 21);
-      const uint32_t tS = tl + L::kSCol + 64 * u, tO = tl + L::kOCol + 128 * u;
+      const uint32_t tO = tl + L::kOCol + 128 * u;
       const int64_t tile = int64_t(h) * tiles + tile_i;
       bool ok = true;
-      if (SHARED || u == 0) {   // the rows' queries to tensor memory
-        const uint8_t* img = a.q_image + tile * (256 * D * (EXACT ? 2 : 1)) + r * 128;
-#pragma unroll 1
-        for (int i = 0; i < L::kPieces * (EXACT ? 2 : 1); ++i) {
-          uint32_t x[32];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 v =
-                *reinterpret_cast<const uint4*>(img + i * L::kQPieceBytes + ((c ^ (r & 7)) << 4));
-            x[4 * c] = v.x;
-            x[4 * c + 1] = v.y;
-            x[4 * c + 2] = v.z;
-            x[4 * c + 3] = v.w;
-          }
-          tmem_st32(tl + L::kQCol + (SHARED ? D / 2 * u : 0) + 32 * i, x);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull[u]);
-      }
       const int rr = min(r0 + r, M - 1);
       const int lim = a.len(rr / g);
       const float f = a.q_factor[tile * kMmaRows + r];
       float ref = -INFINITY, l = 0.0f;       // the reference of the weights, their sum
       for (int m = 0; m < n_mine; ++m) {
         const int j = SHARED ? m : 2 * m + u;
-        if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[u], m & 1, abort_flag, a.guard))) {
+        const uint32_t tS = tl + L::kSCol + 128 * u + 64 * (m & 1);
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sfull[2 * u + (m & 1)], (m >> 1) & 1,
+                                                   abort_flag, a.guard))) {
           ok = false;
           break;
         }
@@ -382,7 +370,10 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         const int tk = t0 + j * TN;
         const uint32_t on[2] = {on_ring[2 * (j & 15)], on_ring[2 * (j & 15) + 1]};
         tmem_wait_ld(s[0], s[1]);
-        if (!__all_sync(0xffffffffu, (on[0] & on[1]) == 0xffffffffu && tk + TN <= lim)) {
+        // a row that ends before this tile needs no mask: its weights are 0 below
+        const bool past = lim <= tk;
+        if (!__all_sync(0xffffffffu,
+                        (on[0] & on[1]) == 0xffffffffu && (past || tk + TN <= lim))) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -397,14 +388,14 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
             mx = max3(mx, __uint_as_float(s[k][i]), __uint_as_float(s[k][i + 1]));
             mx1 = max3(mx1, __uint_as_float(s[k][i + 2]), __uint_as_float(s[k][i + 3]));
           }
-        mx = fmaxf(mx, mx1) * f;             // f > 0
+        mx = past ? -INFINITY : fmaxf(mx, mx1) * f;   // f > 0
         const bool grow = mx > ref + 8.0f || (ref == -INFINITY && mx > -INFINITY);
         const float nref = grow ? mx : ref;
         const float cc = !grow ? 1.0f : ref == -INFINITY ? 0.0f : ex2(ref - nref);
         l *= cc;
         ref = nref;
         // P = 2^7 e^{x - ref} (0 while the row has seen no token)
-        const float b = 7.0f - (ref == -INFINITY ? 0.0f : ref);
+        const float b = past ? -INFINITY : 7.0f - (ref == -INFINITY ? 0.0f : ref);
         float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
         uint32_t ph[32];
         uint32_t pl[EXACT ? 32 : 1];
@@ -425,9 +416,15 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         l += (sum.x + sum.y) + (sum1.x + sum1.y);
         tmem_st32(tS, ph);
         if constexpr (EXACT) tmem_st32(tS + 32, pl);
-        // O follows the reference; these scores came after the values of every
-        // earlier tile of the unit, so it is complete up to there
+        // O follows the reference. These scores were issued after the values of
+        // tile m - 2, so the phase that tells of tile m - 1 is the next or the last.
         if (m > 0 && __any_sync(0xffffffffu, grow)) {
+          if (!__all_sync(0xffffffffu,
+                          wait_or_abort(&odone[u], (m - 1) & 1, abort_flag, a.guard))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < D; k += 32) {
             uint32_t o[32];
@@ -441,7 +438,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[u]);
+        if (lane == 0) mbar_arrive(&pfull[2 * u + (m & 1)]);
       }
       if (ok && __all_sync(0xffffffffu, wait_or_abort(all_done, 0, abort_flag, a.guard))) {
         tc_fence_after();
