@@ -8,7 +8,7 @@ namespace srftq {
 
 // Query rows per KV head from which the prefix goes to the tcgen05 kernel: it
 // computes 128 rows whatever their number, the other kernel 8 at a time.
-constexpr int64_t kMmaMinRows = 24, kMmaMinRowsExact = 48;
+constexpr int64_t kMmaMinRows = 24, kMmaMinRowsExact = 40;
 
 extern template int launch_prefix_tiles<64>(const PrefixArgs&, int, int, cudaStream_t);
 extern template int launch_prefix_tiles<128>(const PrefixArgs&, int, int, cudaStream_t);
@@ -21,7 +21,7 @@ namespace {
 struct PrefixShape {
   bool mma, shared;   // parts by tcgen05; its two units different rows, not alternate tokens
   int32_t splits, per, chunk_goal;
-  int64_t q_off, image_off, factor_off, plan_off, start_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
+  int64_t q_off, image_off, factor_off, plan_off, start_off, chunk_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
 };
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -55,7 +55,7 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
     s.per = int32_t(per);
     s.splits = int32_t((prefix_len + per - 1) / per) * (pair ? 2 : 1);
   }
-  s.chunk_goal = int32_t((4 * int64_t(sms) + heads - 1) / heads);
+  s.chunk_goal = int32_t((8 * int64_t(sms) + heads - 1) / heads);
   const int64_t chunks = s.chunk_goal + n_seq;
   int64_t o = 0;
   auto take = [&](int64_t bytes) {
@@ -69,6 +69,7 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
   s.factor_off = take(padded * 4);
   s.plan_off = take(sizeof(PrefixPlan));
   s.start_off = take((n_seq + 1) * 4);
+  s.chunk_off = take(chunks * 16);
   s.pre_ml_off = take(s.splits * heads * rows * 8);
   s.pre_acc_off = take(s.splits * heads * rows * d * 4);
   s.own_ml_off = take(chunks * heads * g * 8);
@@ -127,6 +128,7 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
   a.q_factor = reinterpret_cast<float*>(ws + s.factor_off);
   a.plan = reinterpret_cast<PrefixPlan*>(ws + s.plan_off);
   a.chunk_start = reinterpret_cast<int32_t*>(ws + s.start_off);
+  a.chunk_of = reinterpret_cast<int4*>(ws + s.chunk_off);
   a.pre_ml = reinterpret_cast<float2*>(ws + s.pre_ml_off);
   a.pre_acc = reinterpret_cast<float*>(ws + s.pre_acc_off);
   a.own_ml = reinterpret_cast<float2*>(ws + s.own_ml_off);

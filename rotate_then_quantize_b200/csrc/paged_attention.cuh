@@ -42,9 +42,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // first chunk of every sequence (chunk c of sequence b covers the own tokens
 // [c chunk, (c + 1) chunk)).
 struct PrefixPlan {
-  int32_t chunk;      // tokens per chunk, a multiple of 64
+  int32_t chunk;      // tokens per chunk, a multiple of 128
   int32_t n_chunks;   // chunks of all sequences
-  int32_t pad[2];
+  int32_t taken;      // items that blocks have taken beyond their first
+  int32_t pad;
 };
 
 struct PrefixArgs {
@@ -77,6 +78,7 @@ struct PrefixArgs {
   float* q_factor;                     // and the rows' score factors, [heads][tiles * 128]
   PrefixPlan* plan;
   int32_t* chunk_start;
+  int4* chunk_of;                      // of each chunk: sequence, first token, end, 0
   float2* pre_ml;                      // [splits][heads][n_seq q_per_kv]
   float* pre_acc;                      // the same rows of d
   float2* own_ml;                      // [chunks][heads][q_per_kv]
@@ -122,9 +124,10 @@ __device__ inline void plan_own_tokens(const PrefixArgs& a) {
   __syncthreads();
   total = 0;
   for (int w = 0; w < nt / 32; ++w) total += total_sh[w];
-  // chunks of at least 64 tokens, few enough that sum ceil(own / chunk) <= goal + n_seq
+  // chunks of at least 128 tokens (a tile for each warp), few enough that
+  // sum ceil(own / chunk) <= goal + n_seq
   const int64_t per = (total + a.chunk_goal - 1) / a.chunk_goal;
-  const int32_t chunk = int32_t(per <= 64 ? 64 : (per + 63) / 64 * 64);
+  const int32_t chunk = int32_t(per <= 128 ? 128 : (per + 127) / 128 * 128);
   int32_t carry = 0;
   for (int b0 = 0; b0 < a.n_seq; b0 += nt) {
     const int b = b0 + tid;
@@ -146,10 +149,18 @@ __device__ inline void plan_own_tokens(const PrefixArgs& a) {
     if (b < a.n_seq) a.chunk_start[b] = before + v - n;
     carry = all;
   }
+  // the chunks' sequences and tokens, so that a block has its next item in one load
+  for (int b = tid; b < a.n_seq; b += nt) {
+    const int32_t end = a.len(b), own = a.own(b);
+    int4* o = a.chunk_of + a.chunk_start[b];   // this thread wrote it
+    for (int32_t c = 0; c * int64_t(chunk) < own; ++c)
+      o[c] = make_int4(b, a.prefix_len + c * chunk, min(a.prefix_len + (c + 1) * chunk, end), 0);
+  }
   if (tid == 0) {
     a.chunk_start[a.n_seq] = carry;
     a.plan->chunk = chunk;
     a.plan->n_chunks = carry;
+    a.plan->taken = 0;
   }
 }
 
@@ -271,7 +282,8 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
 // step is 2^-9), 2^-23 for fp16.
 //
 // Values, O[coord][query] += sum_t (sigma c / 128)[coord][t] p'[t][query], p' =
-// 2^15 e^{x - m} (the factor keeps small weights normal). sigma c / 128 is
+// 2^7 e^{x - m}, m a reference that follows the maximum when that grows by more
+// than 2^8 (the factors keep small weights normal and large ones below 2^15). sigma c / 128 is
 // rounded once to fp16: at most |sigma|, so it never overflows. The 8-bit
 // transposing ldmatrix gives lane (g, t) coordinate g of tokens 4t .. 4t + 3,
 // and the score rows take their tokens in the order that hands the lane's p'
@@ -335,6 +347,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// A constant in a register: (w & mask) ^ magic is one instruction with one
+// immediate and one register, two with two immediates.
+__device__ __forceinline__ uint32_t in_register(uint32_t c) {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(c));
+  return r;
+}
 // 16 bytes of global memory to shared memory, zeros where !on.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -361,7 +380,11 @@ struct TileLayout {
   static constexpr int kStages = 2;
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kMl = kTileWarps * kWarp;             // the warps' (m, l) of 8 rows
-  static constexpr int kBytes = kMl + kTileWarps * 8 * 8;
+  // the item's queries, the same for its warps: right operands by coordinate
+  // group of 16 and lane, hi then lo; float sums [NS16][8 rows]
+  static constexpr int kQf = kMl + kTileWarps * 8 * 8;
+  static constexpr int kQs = kQf + 2 * NS16 * 32 * 8;
+  static constexpr int kBytes = kQs + NS16 * 8 * 4;
   static_assert(kWarp >= 8 * D * 4, "a warp's partial sums fit over its stages");
 };
 
@@ -373,26 +396,24 @@ struct PartItem {
   const int32_t* table;
 };
 
-// Own-token item i: chunk c of a sequence, head h, row tile rt.
-__device__ __forceinline__ PartItem own_item(const PrefixArgs& a, int64_t i, int tiles) {
+// Own-token item i: a chunk of a sequence (rec, of chunk own_chunk()), head h,
+// row tile rt.
+__device__ __forceinline__ int64_t own_chunk(const PrefixArgs& a, int64_t i, int tiles) {
+  return i / (int64_t(tiles) * a.heads);
+}
+__device__ __forceinline__ PartItem own_item(const PrefixArgs& a, int64_t i, int tiles, int4 rec) {
   PartItem p;
   p.pre = false;
   const int rt = int(i % tiles);
   const int64_t q = i / tiles;
   p.h = int(q % a.heads);
-  const int c = int(q / a.heads);
-  int lo = 0, hi = a.n_seq;   // the sequence of chunk c: last start <= c
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.chunk_start + mid) <= c) lo = mid; else hi = mid;
-  }
-  p.b = lo;
+  p.b = rec.x;
   p.r0 = rt * kPrefixRows;
   p.nr = min(kPrefixRows, a.q_per_kv - p.r0);
-  p.t0 = a.prefix_len + (c - a.chunk_start[lo]) * a.plan->chunk;
-  p.t1 = min(p.t0 + a.plan->chunk, a.len(lo));
-  p.part = (int64_t(c) * a.heads + p.h) * a.q_per_kv + p.r0;
-  p.table = a.block_table + int64_t(lo) * a.max_pages;
+  p.t0 = rec.y;
+  p.t1 = rec.z;
+  p.part = q * a.q_per_kv + p.r0;
+  p.table = a.block_table + int64_t(rec.x) * a.max_pages;
   return p;
 }
 // Prefix item i: part s of the prefix, head h, row tile rt.
@@ -415,7 +436,7 @@ __device__ __forceinline__ PartItem pre_item(const PrefixArgs& a, int64_t i, int
 }
 
 template <int D, int BITS, int G, bool EXACT>
-__global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
+__global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 : 5)
     prefix_tile_kernel(const PrefixArgs a) {
   using L = TileLayout<D, BITS, G>;
   constexpr int CB = L::CB, NG = L::NG, NS = L::kStages, S16 = L::NS16, NW = kTileWarps;
@@ -436,8 +457,25 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
   const int own_tiles = (qpk + kPrefixRows - 1) / kPrefixRows;
   const int64_t n_items = n_pre + int64_t(a.plan->n_chunks) * a.heads * own_tiles;
 
-  for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
-    const PartItem p = it < n_pre ? pre_item(a, it, pre_tiles) : own_item(a, it - n_pre, own_tiles);
+  // A block takes the next item when it is done with one: sequences differ in
+  // length, and which block does an item changes nothing in it.
+  __shared__ int32_t next_sh;
+  __shared__ int4 rec_sh;
+  auto record = [&](int64_t i) {
+    return i >= n_pre && i < n_items ? __ldg(a.chunk_of + own_chunk(a, i - n_pre, own_tiles))
+                                     : make_int4(0, 0, 0, 0);
+  };
+  int4 rec = record(blockIdx.x);
+  for (int64_t it = blockIdx.x; it < n_items;) {
+    const PartItem p =
+        it < n_pre ? pre_item(a, it, pre_tiles) : own_item(a, it - n_pre, own_tiles, rec);
+    // the next item and its record are on their way while this one is done
+    int32_t next = 0;
+    int4 next_rec;
+    if (threadIdx.x == 0) {
+      next = atomicAdd(&a.plan->taken, 1);
+      next_rec = record(int64_t(gridDim.x) + next);
+    }
     const int n_chunks = max(0, (p.t1 - p.t0 - kTileChunk * warp + kTileChunk * NW - 1) /
                                     (kTileChunk * NW));
     // zero the unused part of the scale rows (partial sums lay there before)
@@ -495,64 +533,66 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
 #pragma unroll
     for (int c = 0; c < NS - 1; ++c) issue(c, row_at[c]);
 
-    // this lane's part of query g: coordinates 16 s + 4 t .. + 3
+    // query g, this lane's coordinates 16 s + 4 t .. + 3: every warp finds the
+    // row's scale, each makes the operands of every fourth s
     const int rq = p.r0 + min(g, p.nr - 1);
     const int bq = p.pre ? rq / qpk : p.b;
     const float* qv = a.qrot + (int64_t(bq) * hq + p.h * qpk + (p.pre ? rq % qpk : rq)) * D;
-    float4 qf[S16];
     float amax = 0.0f;
 #pragma unroll
     for (int s = 0; s < S16; ++s) {
-      qf[s] = __ldg(reinterpret_cast<const float4*>(qv + 16 * s + 4 * t));
-      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(qf[s].x), fabsf(qf[s].y)),
-                               fmaxf(fabsf(qf[s].z), fabsf(qf[s].w))));
+      const float4 x = __ldg(reinterpret_cast<const float4*>(qv + 16 * s + 4 * t));
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const int e = query_exponent(amax);
     const float up = __uint_as_float(uint32_t(e + 127) << 23);
-    uint32_t qh[S16][2], ql[EXACT ? S16 : 1][2];
-    float gsum[NG];
+    const uint32_t qf = smem_addr(smem + L::kQf) + lane * 8;
+    float* qsum = reinterpret_cast<float*>(smem + L::kQs);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) gsum[i] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < S16; ++s) {
+    for (int i = 0; i < S16 / NW; ++i) {
+      const int s = warp + NW * i;
+      const float4 x = __ldg(reinterpret_cast<const float4*>(qv + 16 * s + 4 * t));
       constexpr float odd = BITS == 4 ? 0.0625f : 1.0f;   // int4: odd coordinates' codes are 16 u
-      const float x0 = qf[s].x * up, x1 = qf[s].y * up, x2 = qf[s].z * up, x3 = qf[s].w * up;
-      qh[s][0] = pack_half2(x0, x2);
-      qh[s][1] = pack_half2(x1 * odd, x3 * odd);
-      float2 f0 = unpack_half2(qh[s][0]), f1 = unpack_half2(qh[s][1]);
+      const float x0 = x.x * up, x1 = x.y * up * odd, x2 = x.z * up, x3 = x.w * up * odd;
+      const uint2 hi = make_uint2(pack_half2(x0, x2), pack_half2(x1, x3));
+      sts64(qf + s * 256, hi);
+      float2 f0 = unpack_half2(hi.x), f1 = unpack_half2(hi.y);
       if constexpr (EXACT) {
-        ql[s][0] = pack_half2(x0 - f0.x, x2 - f0.y);
-        ql[s][1] = pack_half2(x1 * odd - f1.x, x3 * odd - f1.y);
-        const float2 l0 = unpack_half2(ql[s][0]), l1 = unpack_half2(ql[s][1]);
+        const uint2 lo = make_uint2(half2_rest(x0, x2, hi.x), half2_rest(x1, x3, hi.y));
+        sts64(qf + (S16 + s) * 256, lo);
+        const float2 l0 = unpack_half2(lo.x), l1 = unpack_half2(lo.y);
         f0 = make_float2(f0.x + l0.x, f0.y + l0.y);
         f1 = make_float2(f1.x + l1.x, f1.y + l1.y);
       }
-      gsum[16 * s / G] += (f0.x + f0.y) + (f1.x + f1.y) * (1.0f / odd);
+      float sum = (f0.x + f0.y) + (f1.x + f1.y) * (1.0f / odd);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (t == 0) qsum[8 * s + g] = sum;
     }
-    // offsets of groups 2t, 2t + 1 (+ 8 i) as fp16 hi and lo: -(8 or 128) 2^-24 sum q
+    __syncthreads();
+    // offsets of groups 2t, 2t + 1 (+ 8 o) as fp16 hi and lo: -(8 or 128) 2^-24 sum q
     constexpr int NO = NG > 8 ? NG / 8 : 1;
     uint32_t off[NO][2];
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      gsum[i] += __shfl_xor_sync(0xffffffffu, gsum[i], 1);
-      gsum[i] += __shfl_xor_sync(0xffffffffu, gsum[i], 2);
-      gsum[i] *= BITS == 4 ? -0x1p-21f : -0x1p-17f;
-    }
-#pragma unroll
     for (int o = 0; o < NO; ++o) {
-      float x0 = 0.0f, x1 = 0.0f;
+      float x[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < 8 && 8 * o + i < NG; ++i) {
-        if (i / 2 == t) (i % 2 ? x1 : x0) = gsum[8 * o + i];
+      for (int k = 0; k < 2; ++k) {
+        const int gi = 8 * o + 2 * t + k;
+        if (gi < NG) {
+#pragma unroll
+          for (int i = 0; i < G / 16; ++i) x[k] += qsum[8 * (gi * (G / 16) + i) + g];
+        }
+        x[k] *= BITS == 4 ? -0x1p-21f : -0x1p-17f;
       }
-      off[o][0] = pack_half2(x0, x1);
-      off[o][1] = half2_rest(x0, x1, off[o][0]);
+      off[o][0] = pack_half2(x[0], x[1]);
+      off[o][1] = half2_rest(x[0], x[1], off[o][0]);
     }
     // columns 2t and 2t + 1 of the score tile: their factor, token limit
     const float down = __uint_as_float(uint32_t(127 - e) << 23) * 0x1p24f;
-    const int lim_g = a.len(bq);
+    const int lim_g = p.pre ? a.len(bq) : p.t1;
     float fs[2];
     int lim[2];
 #pragma unroll
@@ -561,7 +601,13 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
       lim[c] = __shfl_sync(0xffffffffu, lim_g, 8 * t + 4 * c);
     }
 
+    // u of even and odd coordinates as fp16 subnormals; 1024 + u, 1024 + 16 u
+    const uint32_t u_lo = in_register(BITS == 4 ? 0x00080008u : 0x00800080u);
+    const uint32_t u_hi = in_register(0x00800080u);
+    const uint32_t h_lo = in_register(BITS == 4 ? 0x64086408u : 0x64806480u);
+    const uint32_t h_hi = in_register(0x64806480u);
     float O[S16][4];
+    // per column the reference of the weights (within 2^8 of the maximum), their sum
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < S16; ++s)
@@ -615,19 +661,23 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
               const uint32_t sel = t & 1 ? 0x4342u : 0x4140u;
               const uint32_t y0 = __byte_perm(lds32(k0 + 8 * s + 4 * (t >> 1)), 0u, sel);
               const uint32_t y1 = __byte_perm(lds32(k1 + 8 * s + 4 * (t >> 1)), 0u, sel);
-              a0 = (y0 & 0x000F000Fu) ^ 0x00080008u;
-              a1 = (y1 & 0x000F000Fu) ^ 0x00080008u;
-              a2 = (y0 & 0x00F000F0u) ^ 0x00800080u;
-              a3 = (y1 & 0x00F000F0u) ^ 0x00800080u;
+              a0 = (y0 & 0x000F000Fu) ^ u_lo;
+              a1 = (y1 & 0x000F000Fu) ^ u_lo;
+              a2 = (y0 & 0x00F000F0u) ^ u_hi;
+              a3 = (y1 & 0x00F000F0u) ^ u_hi;
             } else {
               const uint32_t y0 = lds32(k0 + 16 * s + 4 * t), y1 = lds32(k1 + 16 * s + 4 * t);
-              a0 = (y0 & 0x00FF00FFu) ^ 0x00800080u;
-              a1 = (y1 & 0x00FF00FFu) ^ 0x00800080u;
-              a2 = ((y0 >> 8) & 0x00FF00FFu) ^ 0x00800080u;
-              a3 = ((y1 >> 8) & 0x00FF00FFu) ^ 0x00800080u;
+              a0 = (y0 & 0x00FF00FFu) ^ u_lo;
+              a1 = (y1 & 0x00FF00FFu) ^ u_lo;
+              a2 = ((y0 >> 8) & 0x00FF00FFu) ^ u_lo;
+              a3 = ((y1 >> 8) & 0x00FF00FFu) ^ u_lo;
             }
-            mma_f16(acc, a0, a1, a2, a3, qh[s][0], qh[s][1]);
-            if constexpr (EXACT) mma_f16(acc, a0, a1, a2, a3, ql[s][0], ql[s][1]);
+            const uint2 qh = lds64(qf + s * 256);
+            mma_f16(acc, a0, a1, a2, a3, qh.x, qh.y);
+            if constexpr (EXACT) {
+              const uint2 ql = lds64(qf + (S16 + s) * 256);
+              mma_f16(acc, a0, a1, a2, a3, ql.x, ql.y);
+            }
           }
           S[mt][0] = fmaf(sg0[gi], acc[0], S[mt][0]);
           S[mt][1] = fmaf(sg0[gi], acc[1], S[mt][1]);
@@ -659,10 +709,11 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
         mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
         mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
       }
-      const float mn0 = fmaxf(m[0], mx[0]), mn1 = fmaxf(m[1], mx[1]);
-      if (__any_sync(0xffffffffu, mn0 > m[0] || mn1 > m[1])) {
-        const float al0 = m[0] == -INFINITY ? 0.0f : ex2(m[0] - mn0);
-        const float al1 = m[1] == -INFINITY ? 0.0f : ex2(m[1] - mn1);
+      const bool g0 = mx[0] > m[0] + 8.0f || (m[0] == -INFINITY && mx[0] > -INFINITY);
+      const bool g1 = mx[1] > m[1] + 8.0f || (m[1] == -INFINITY && mx[1] > -INFINITY);
+      if (__any_sync(0xffffffffu, g0 || g1)) {
+        const float al0 = !g0 ? 1.0f : m[0] == -INFINITY ? 0.0f : ex2(m[0] - mx[0]);
+        const float al1 = !g1 ? 1.0f : m[1] == -INFINITY ? 0.0f : ex2(m[1] - mx[1]);
         l[0] *= al0;
         l[1] *= al1;
 #pragma unroll
@@ -672,12 +723,12 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
           O[s][2] *= al0;
           O[s][3] *= al1;
         }
-        m[0] = mn0;
-        m[1] = mn1;
+        if (g0) m[0] = mx[0];
+        if (g1) m[1] = mx[1];
       }
-      // p' = 2^15 e^{x - m}; without any token yet the reference is 0 and p' = 0
-      const float b0 = (m[0] == -INFINITY ? 0.0f : m[0]) - 15.0f;
-      const float b1 = (m[1] == -INFINITY ? 0.0f : m[1]) - 15.0f;
+      // p' = 2^7 e^{x - m}; without any token yet the reference is 0 and p' = 0
+      const float b0 = (m[0] == -INFINITY ? 0.0f : m[0]) - 7.0f;
+      const float b1 = (m[1] == -INFINITY ? 0.0f : m[1]) - 7.0f;
       uint32_t ph[2][2], pl[2][2];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
@@ -729,10 +780,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t y = r[i] >> 8;
-              weigh(s + i, hfma2((r[i] & 0x000F000Fu) ^ 0x64086408u, k128, o8),
-                    hfma2((r[i] & 0x00F000F0u) ^ 0x64806480u, k128, o128),
-                    hfma2((y & 0x000F000Fu) ^ 0x64086408u, k128, o8),
-                    hfma2((y & 0x00F000F0u) ^ 0x64806480u, k128, o128));
+              weigh(s + i, hfma2((r[i] & 0x000F000Fu) ^ h_lo, k128, o8),
+                    hfma2((r[i] & 0x00F000F0u) ^ h_hi, k128, o128),
+                    hfma2((y & 0x000F000Fu) ^ h_lo, k128, o8),
+                    hfma2((y & 0x00F000F0u) ^ h_hi, k128, o128));
             }
           }
         } else {
@@ -740,10 +791,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
           for (int s = 0; s < S16; ++s) {
             uint32_t r0, r1;
             ldmatrix_bytes_trans(r0, r1, vr + 16 * s);
-            weigh(s, hfma2((r0 & 0x00FF00FFu) ^ 0x64806480u, k128, o128),
-                  hfma2((r1 & 0x00FF00FFu) ^ 0x64806480u, k128, o128),
-                  hfma2(((r0 >> 8) & 0x00FF00FFu) ^ 0x64806480u, k128, o128),
-                  hfma2(((r1 >> 8) & 0x00FF00FFu) ^ 0x64806480u, k128, o128));
+            weigh(s, hfma2((r0 & 0x00FF00FFu) ^ h_lo, k128, o128),
+                  hfma2((r1 & 0x00FF00FFu) ^ h_lo, k128, o128),
+                  hfma2(((r0 >> 8) & 0x00FF00FFu) ^ h_lo, k128, o128),
+                  hfma2(((r1 >> 8) & 0x00FF00FFu) ^ h_lo, k128, o128));
           }
         }
       }
@@ -760,12 +811,12 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
       l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
     }
     if (g == 0) {
-      ml_sh[warp][2 * t] = make_float2(m[0], l[0] * 0x1p-15f);
-      ml_sh[warp][2 * t + 1] = make_float2(m[1], l[1] * 0x1p-15f);
+      ml_sh[warp][2 * t] = make_float2(m[0], l[0] * 0x1p-7f);
+      ml_sh[warp][2 * t + 1] = make_float2(m[1], l[1] * 0x1p-7f);
     }
 #pragma unroll
     for (int s = 0; s < S16; ++s) {
-      constexpr float f0 = 0x1p-8f, f1 = BITS == 4 ? 0x1p-12f : 0x1p-8f;   // 128 / 2^15 (/ 16)
+      constexpr float f0 = 1.0f, f1 = BITS == 4 ? 0.0625f : 1.0f;   // 128 / 2^7 (/ 16)
       if constexpr (BITS == 4) {   // rows g, g + 8: coordinates 2g, 2g + 1
         float* o = wo + 2 * t * D + 16 * s + 2 * g;
         *reinterpret_cast<float2*>(o) = make_float2(O[s][0] * f0, O[s][2] * f1);
@@ -778,7 +829,13 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : EXACT ? 3 : 4)
         o[D + 8] = O[s][3] * f1;
       }
     }
+    if (threadIdx.x == 0) {
+      next_sh = next;
+      rec_sh = next_rec;
+    }
     __syncthreads();
+    it = int64_t(gridDim.x) + next_sh;
+    rec = rec_sh;
     float* to_acc = p.pre ? a.pre_acc : a.own_acc;
     float2* to_ml = p.pre ? a.pre_ml : a.own_ml;
     for (int i = threadIdx.x; i < p.nr * (D / 4); i += NW * 32) {
