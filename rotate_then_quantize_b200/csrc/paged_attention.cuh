@@ -73,6 +73,7 @@ struct PrefixArgs {
   bool pre_mma;                        // the prefix's parts come from a tcgen05 kernel
   bool pre_shared;                     // whose two units are different rows (prefix_pair.cuh)
   int32_t bits;
+  uint32_t zero;                       // 0 (in_register)
   float* qrot;                         // workspace: rotated queries
   uint8_t* q_image;                    // pre_mma: the rows' fp16 tiles, [heads][tiles] of them
   float* q_factor;                     // and the rows' score factors, [heads][tiles * 128]
@@ -347,13 +348,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// A constant in a register: (w & mask) ^ magic is one instruction with one
-// immediate and one register, two with two immediates.
-__device__ __forceinline__ uint32_t in_register(uint32_t c) {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(c));
-  return r;
-}
+// A constant in a register (zero is a kernel argument that is 0, so that it
+// cannot be folded): (w & mask) ^ magic is one instruction with one immediate and
+// one register, two with two immediates.
+__device__ __forceinline__ uint32_t in_register(uint32_t c, uint32_t zero) { return c ^ zero; }
 // 16 bytes of global memory to shared memory, zeros where !on.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -602,10 +600,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     }
 
     // u of even and odd coordinates as fp16 subnormals; 1024 + u, 1024 + 16 u
-    const uint32_t u_lo = in_register(BITS == 4 ? 0x00080008u : 0x00800080u);
-    const uint32_t u_hi = in_register(0x00800080u);
-    const uint32_t h_lo = in_register(BITS == 4 ? 0x64086408u : 0x64806480u);
-    const uint32_t h_hi = in_register(0x64806480u);
+    const uint32_t u_lo = in_register(BITS == 4 ? 0x00080008u : 0x00800080u, a.zero);
+    const uint32_t u_hi = in_register(0x00800080u, a.zero);
+    const uint32_t h_lo = in_register(BITS == 4 ? 0x64086408u : 0x64806480u, a.zero);
+    const uint32_t h_hi = in_register(0x64806480u, a.zero);
     float O[S16][4];
     // per column the reference of the weights (within 2^8 of the maximum), their sum
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};

@@ -78,23 +78,25 @@ __host__ __device__ constexpr bool decoded_times16(int p) {
 }
 
 // 8 codes (1 or 2 words) to sigma c / 128 in decoded order: v rounded to fp16,
-// rest what that left (exact, but for subnormals).
+// rest what that left (exact, but for subnormals). h_lo, h_hi: the magic numbers
+// 1024 + u and 1024 + 16 u in registers.
 template <int BITS, bool REST>
-__device__ __forceinline__ void decode_chunk(const uint32_t* w, uint32_t sg2, uint4& v, uint4& rest) {
+__device__ __forceinline__ void decode_chunk(const uint32_t* w, uint32_t sg2, uint32_t h_lo,
+                                             uint32_t h_hi, uint4& v, uint4& rest) {
   constexpr uint32_t k128 = 0x20002000u;                     // 2^-7
   constexpr uint32_t o8 = 0xC808C808u, o128 = 0xC880C880u;   // -1032 / 128, -1152 / 128
   uint32_t c[4];
   if constexpr (BITS == 4) {
     const uint32_t y = w[0] >> 8;
-    c[0] = hfma2((w[0] & 0x000F000Fu) ^ 0x64086408u, k128, o8);
-    c[1] = hfma2((w[0] & 0x00F000F0u) ^ 0x64806480u, k128, o128);
-    c[2] = hfma2((y & 0x000F000Fu) ^ 0x64086408u, k128, o8);
-    c[3] = hfma2((y & 0x00F000F0u) ^ 0x64806480u, k128, o128);
+    c[0] = hfma2((w[0] & 0x000F000Fu) ^ h_lo, k128, o8);
+    c[1] = hfma2((w[0] & 0x00F000F0u) ^ h_hi, k128, o128);
+    c[2] = hfma2((y & 0x000F000Fu) ^ h_lo, k128, o8);
+    c[3] = hfma2((y & 0x00F000F0u) ^ h_hi, k128, o128);
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      c[2 * i] = hfma2((w[i] & 0x00FF00FFu) ^ 0x64806480u, k128, o128);
-      c[2 * i + 1] = hfma2(((w[i] >> 8) & 0x00FF00FFu) ^ 0x64806480u, k128, o128);
+      c[2 * i] = hfma2((w[i] & 0x00FF00FFu) ^ h_hi, k128, o128);
+      c[2 * i + 1] = hfma2(((w[i] >> 8) & 0x00FF00FFu) ^ h_hi, k128, o128);
     }
   }
   v = make_uint4(hmul2(c[0], sg2), hmul2(c[1], sg2), hmul2(c[2], sg2), hmul2(c[3], sg2));
@@ -110,7 +112,8 @@ __device__ __forceinline__ void decode_chunk(const uint32_t* w, uint32_t sg2, ui
 // start at different chunks (order j ^ rot).
 template <int D, int BITS, int G, int TN, bool REST, int NK>
 __device__ __forceinline__ void decode_pieces(uint32_t base, uint32_t rest_at, int pc, int tr,
-                                              const uint4 (&w)[NK], const uint32_t (&s)[NK]) {
+                                              const uint4 (&w)[NK], const uint32_t (&s)[NK],
+                                              uint32_t h_lo, uint32_t h_hi) {
   constexpr int PPT = D * BITS / 128, RPP = 128 / PPT, NC = 16 / BITS;
   constexpr bool TWO = 128 / BITS > G;   // two scales to a piece
   const int rot = BITS == 4 ? (PPT == 4 ? (pc >> 1) * 2 : PPT == 8 ? pc >> 1 : 0)
@@ -142,7 +145,7 @@ __device__ __forceinline__ void decode_pieces(uint32_t base, uint32_t rest_at, i
       const int c = pc * NC + (j ^ rot);
       const uint32_t at = base + (c >> 3) * (TN * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
       uint4 v, r;
-      decode_chunk<BITS, REST>(x + j * 4 / NC, 2 * j < NC ? s0 : s1, v, r);
+      decode_chunk<BITS, REST>(x + j * 4 / NC, 2 * j < NC ? s0 : s1, h_lo, h_hi, v, r);
       sts128(at, v);
       if constexpr (REST) sts128(at + rest_at, r);
     }
@@ -269,6 +272,8 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
     static_assert(TN % RPP == 0 && GC <= 2, "pieces");
     const int dt = tid - 128;
     const int pc = dt % PPT, tr = dt / PPT;
+    const uint32_t h_lo = in_register(0x64086408u, a.zero);
+    const uint32_t h_hi = in_register(0x64806480u, a.zero);
     uint4 kw[NK], vw[NK];
     uint32_t ks[NK], vs[NK];
     int32_t page[NK], row[NK], next[NK];   // table entry two steps on; rows of this step, the next
@@ -317,7 +322,8 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
 #pragma unroll
         for (int k = 0; k < NK; ++k) on_sh[(i & 3) * TN + tr + k * RPP] = row[k] >= 0 ? 1 : 0;
       }
-      decode_pieces<D, BITS, G, TN, EXACT, NK>(sm + L::kKOff + st * L::kKT, L::kT, pc, tr, kw, ks);
+      decode_pieces<D, BITS, G, TN, EXACT, NK>(sm + L::kKOff + st * L::kKT, L::kT, pc, tr, kw, ks, h_lo,
+                                           h_hi);
       __threadfence_block();
       fence_proxy_async_smem();
       __syncwarp();
@@ -326,7 +332,8 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
       if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&vempty[st], ((i >> 1) & 1) ^ 1,
                                                            abort_flag, a.guard)))
         break;
-      decode_pieces<D, BITS, G, TN, false, NK>(sm + L::kVOff + st * L::kT, 0, pc, tr, vw, vs);
+      decode_pieces<D, BITS, G, TN, false, NK>(sm + L::kVOff + st * L::kT, 0, pc, tr, vw, vs, h_lo,
+                                           h_hi);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&vfull[st]);

@@ -290,6 +290,8 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
     constexpr int NK = TN / RPP, CC = 128 / BITS;        // pieces of a thread, coordinates of one
     constexpr bool TWO = CC > G;                         // two scales to a piece
     const int dt = tid - 256, pc = dt % PPT, tr = dt / PPT;
+    const uint32_t h_lo = in_register(0x64086408u, a.zero);
+    const uint32_t h_hi = in_register(0x64806480u, a.zero);
     uint4 w[NK];
     uint32_t s[NK];
     auto fetch = [&](uint32_t codes, uint32_t scales) {
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
       if (j >= NS && !__all_sync(0xffffffffu, wait_or_abort(&kempty[sl], ((j / NS) & 1) ^ 1,
                                                             abort_flag, a.guard)))
         break;
-      decode_pieces<D, BITS, G, TN, EXACT, NK>(tb, L::kT, pc, tr, w, s);
+      decode_pieces<D, BITS, G, TN, EXACT, NK>(tb, L::kT, pc, tr, w, s, h_lo, h_hi);
       fetch(rb + L::kRawV, rb + L::kRawVS);
       fence_proxy_async_smem();
       __syncwarp();
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
       if (j >= NS && !__all_sync(0xffffffffu, wait_or_abort(&vempty[sl], ((j / NS) & 1) ^ 1,
                                                             abort_flag, a.guard)))
         break;
-      decode_pieces<D, BITS, G, TN, false, NK>(tb + L::kKT, 0, pc, tr, w, s);
+      decode_pieces<D, BITS, G, TN, false, NK>(tb + L::kKT, 0, pc, tr, w, s, h_lo, h_hi);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&vfull[sl]);
