@@ -41,11 +41,12 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
     const int64_t tile = s.shared ? 2 * kMmaRows : s.mma ? kMmaRows : kPrefixRows;
     const int64_t units = (rows + tile - 1) / tile * heads;
     const int64_t over = s.mma ? 512 : 128;
+    const int64_t join = (4 + rows * heads * d / 10000) * (pair ? 2 : 1);
     int64_t best = 0, best_n = 1;
     const int64_t most = (prefix_len + 63) / 64;
     for (int64_t n = 1; n <= most && units * n <= 4 * slots + units; n += n / 16 + 1) {
       const int64_t per = ((prefix_len + n - 1) / n + 63) / 64 * 64;
-      const int64_t cost = (units * n + slots - 1) / slots * (per + over) + 4 * n;
+      const int64_t cost = (units * n + slots - 1) / slots * (per + over) + n * join;
       if (best == 0 || cost < best) {
         best = cost;
         best_n = n;

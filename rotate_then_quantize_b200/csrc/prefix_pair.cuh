@@ -14,9 +14,9 @@
 //            softmax (up to 128 rows, and fp16 outputs).
 //
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, a query row per thread. Warps
-// 8-11: codes to fp16 tiles (swizzled, sigma c / 128 rounded once: at most
-// |sigma|, so it cannot overflow). Warps 12 and 13: issue the units' products.
-// Warps 14 and 15: copy codes and scales of one tile each in turn into a ring of
+// 8-11 and 12-15: codes of keys and of values to fp16 tiles (swizzled, sigma c /
+// 128 rounded once: at most |sigma|, so it cannot overflow). Warps 16 and 17:
+// issue the units' products. Warps 18 and 19: copy codes and scales of one tile each in turn into a ring of
 // raw stages, so that memory latency is hidden by depth, not by registers. O is rescaled only
 // when a row's maximum grows by more than 2^8 over the reference its weights use
 // (the weights stay below 2^15; the final quotient does not see the reference).
@@ -61,7 +61,7 @@ struct PrefixPair {
   static constexpr int kBytes = kBarOff + 8 * kBars + 16;
   static constexpr int kSmem = kBytes + 1024;                       // slack to start on 1024 bytes
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static constexpr int kThreads = 512;
+  static constexpr int kThreads = 640;
   static constexpr int kQPiece = kMmaRows * 128;                    // a piece of a query tile
   // tensor memory columns: score tiles (two of each unit), accumulators
   static constexpr int kSCol = 0, kOCol = 256;
@@ -77,7 +77,7 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
 }
 
 template <int D, int BITS, int G, bool EXACT, bool SHARED>
-__global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a) {
   using L = PrefixPair<D, BITS, G, EXACT, SHARED>;
   constexpr int TN = L::TN, CB = L::CB, NG = L::NG, NS = L::kSlots, NR = L::kRaws;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
   if (tid == 0) {
     for (int i = 0; i < NR; ++i) {
       mbar_init(&rfull[i], 33);
-      mbar_init(&rempty[i], 4);
+      mbar_init(&rempty[i], 8);
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&kfull[i], 4);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
   grid_dependency_wait();   // the query tiles
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 12 || warp == 13) {
+  if (warp == 16 || warp == 17) {
     // ---------------- MMA issuers, one for each unit ----------------
     // The whole warp runs this and every operand is the same in its lanes, so
     // addresses and descriptors stay in uniform registers; one elected lane
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         }
         tc_commit_elect(&odone[u]);
       };
-      const int u = warp - 12;
+      const int u = warp - 16;
       const int n_mine = u < units ? (SHARED ? n : (n + 1 - u) / 2) : 0;
       uint64_t* my_q = &qfull[SHARED ? u : 0];
       if (lane == 0 && (SHARED ? u < units : u == 0)) {
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
       (void)mbar_wait_bounded(all_done, 0);
       __syncwarp();
     }
-  } else if (warp > 13) {
-    // ---------------- loaders: tile j by warp 14 + j % 2 ----------------
+  } else if (warp > 17) {
+    // ---------------- loaders: tile j by warp 18 + j % 2 ----------------
     constexpr int PPT = CB / 16, NK = TN * PPT / 32;   // pieces of a row, of a lane
     int32_t page[2];
     auto look_up = [&](int j) {
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         page[k] = j < n && t < t1 ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t))) : -1;
       }
     };
-    look_up(warp - 14);
-    for (int j = warp - 14; j < n; j += 2) {
+    look_up(warp - 18);
+    for (int j = warp - 18; j < n; j += 2) {
       const int st = j % NR;
       int32_t row[2];
 #pragma unroll
@@ -284,21 +284,31 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= 8) {
-    // ---------------- codes to fp16 tiles ----------------
+    // ---------------- codes to fp16 tiles: warps 8-11 keys, 12-15 values ----------------
     // Neighbouring threads take the 16-byte pieces of one row.
     constexpr int PPT = CB / 16, RPP = 128 / PPT;        // pieces of a row, rows per pass
     constexpr int NK = TN / RPP, CC = 128 / BITS;        // pieces of a thread, coordinates of one
     constexpr bool TWO = CC > G;                         // two scales to a piece
-    const int dt = tid - 256, pc = dt % PPT, tr = dt / PPT;
+    const bool keys = warp < 12;
+    const int dt = tid & 127, pc = dt % PPT, tr = dt / PPT;
     const uint32_t h_lo = in_register(0x64086408u, a.zero);
     const uint32_t h_hi = in_register(0x64806480u, a.zero);
-    uint4 w[NK];
-    uint32_t s[NK];
-    auto fetch = [&](uint32_t codes, uint32_t scales) {
+    uint64_t *full = keys ? kfull : vfull, *empty = keys ? kempty : vempty;
+    const uint32_t codes = sm + L::kRawOff + (keys ? 0 : L::kRawV) + dt * 16;
+    const uint32_t scales = sm + L::kRawOff + (keys ? L::kRawKS : L::kRawVS) + tr * L::SBS +
+                            pc * CC / G * 2;
+    const uint32_t tiles_at = sm + L::kSlotOff + (keys ? 0 : L::kKT);
+    for (int j = 0; j < n; ++j) {
+      const int st = j % NR, sl = j % NS;
+      if (!__all_sync(0xffffffffu,
+                      wait_or_abort(&rfull[st], (j / NR) & 1, abort_flag, a.guard)))
+        break;
+      uint4 w[NK];
+      uint32_t s[NK];
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        w[k] = lds128(codes + (dt + 128 * k) * 16);
-        const uint32_t sa = scales + (tr + k * RPP) * L::SBS + pc * CC / G * 2;
+        w[k] = lds128(codes + st * L::kRawStage + 2048 * k);
+        const uint32_t sa = scales + st * L::kRawStage + k * RPP * L::SBS;
         if constexpr (TWO) {
           s[k] = lds32(sa);
         } else {
@@ -307,15 +317,6 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
           s[k] = x;
         }
       }
-    };
-    for (int j = 0; j < n; ++j) {
-      const int st = j % NR, sl = j % NS;
-      if (!__all_sync(0xffffffffu,
-                      wait_or_abort(&rfull[st], (j / NR) & 1, abort_flag, a.guard)))
-        break;
-      const uint32_t rb = sm + L::kRawOff + st * L::kRawStage;
-      const uint32_t tb = sm + L::kSlotOff + sl * L::kSlot;
-      fetch(rb, rb + L::kRawKS);
       // an entry of the ring is written again 16 tiles on, long after the
       // softmax of this tile: at most the slots' tiles lie between
       if (tid == 256) {
@@ -323,24 +324,21 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         on_ring[2 * (j & 15) + 1] = on_raw[2 * st + 1];
         __threadfence_block();
       }
-      if (j >= NS && !__all_sync(0xffffffffu, wait_or_abort(&kempty[sl], ((j / NS) & 1) ^ 1,
+      if (j >= NS && !__all_sync(0xffffffffu, wait_or_abort(&empty[sl], ((j / NS) & 1) ^ 1,
                                                             abort_flag, a.guard)))
         break;
-      decode_pieces<D, BITS, G, TN, EXACT, NK>(tb, L::kT, pc, tr, w, s, h_lo, h_hi);
-      fetch(rb + L::kRawV, rb + L::kRawVS);
+      if (EXACT && keys)
+        decode_pieces<D, BITS, G, TN, EXACT, NK>(tiles_at + sl * L::kSlot, L::kT, pc, tr, w, s, h_lo,
+                                                 h_hi);
+      else
+        decode_pieces<D, BITS, G, TN, false, NK>(tiles_at + sl * L::kSlot, 0, pc, tr, w, s, h_lo,
+                                                 h_hi);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&kfull[sl]);
+        mbar_arrive(&full[sl]);
         mbar_arrive(&rempty[st]);
       }
-      if (j >= NS && !__all_sync(0xffffffffu, wait_or_abort(&vempty[sl], ((j / NS) & 1) ^ 1,
-                                                            abort_flag, a.guard)))
-        break;
-      decode_pieces<D, BITS, G, TN, false, NK>(tb + L::kKT, 0, pc, tr, w, s, h_lo, h_hi);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&vfull[sl]);
     }
   } else {
     // ---------------- softmax: a query row per thread ----------------
@@ -399,10 +397,9 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
         // P = 2^7 e^{x - ref} (0 while the row has seen no token)
         const float b = past ? -INFINITY : 7.0f - (ref == -INFINITY ? 0.0f : ref);
         float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
-        uint32_t ph[32];
-        uint32_t pl[EXACT ? 32 : 1];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {   // 32 tokens at a time, to free their scores
+          uint32_t ph[16], pl[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float2 x = __ffma2_rn(
@@ -412,12 +409,13 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
             if (i & 2) sum1 = __fadd2_rn(sum1, p);
             else sum = __fadd2_rn(sum, p);
             const uint32_t hh = pack_half2(p.x, p.y);
-            ph[16 * k + i / 2] = hh;
-            if constexpr (EXACT) pl[16 * k + i / 2] = half2_rest(p.x, p.y, hh);
+            ph[i / 2] = hh;
+            if constexpr (EXACT) pl[i / 2] = half2_rest(p.x, p.y, hh);
           }
+          tmem_st16(tS + 16 * k, ph);
+          if constexpr (EXACT) tmem_st16(tS + 32 + 16 * k, pl);
+        }
         l += (sum.x + sum.y) + (sum1.x + sum1.y);
-        tmem_st32(tS, ph);
-        if constexpr (EXACT) tmem_st32(tS + 32, pl);
         // O follows the reference. These scores were issued after the values of
         // tile m - 2, so the phase that tells of tile m - 1 is the next or the last.
         if (m > 0 && __any_sync(0xffffffffu, grow)) {
@@ -474,7 +472,7 @@ __global__ void __launch_bounds__(512, 1) prefix_pair_kernel(const PrefixArgs a)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace srftq
