@@ -107,8 +107,7 @@ def test_paged_codec(N, H, holes, d, bits, group, rot):
     other row of the pools keeps its bytes; reading back gives the oracle's
     dequantisation, and rows without a slot keep theirs."""
     import torch
-    if N * H * d > 10 ** 6:
-        pytest.skip("the oracle's share of the time")
+    N = min(N, 10 ** 6 // (H * d))   # the oracle's share of the time
     rng = np.random.default_rng(N * 31 + H * 7 + d + bits + group + rot)
     S, rows = 2, N + 13
     x = rng.standard_normal((S, N, H, d))
@@ -432,6 +431,97 @@ def test_other_stream_and_graphs():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want.flip(0))
+
+
+@pytest.mark.parametrize("dtype,n_seq,d", [("bfloat16", 40, 128), ("float16", 20, 64),
+                                           ("float16", 3, 128), ("bfloat16", 12, 256)])
+def test_one_workspace_for_calls_in_turn(dtype, n_seq, d):
+    """Calls in a stream may share a workspace: two batches in turn, thirty
+    times without a wait between, with the results they have by themselves."""
+    import torch
+    rng = np.random.default_rng(20)
+    cases = [_attn_case(rng, n_seq, 2, 4, d, 4, 16, 0, 300, _ragged(rng, n_seq, 200 - 150 * i), 16,
+                        dtype)[:2] for i in range(2)]
+    want = [rq.prefix_attention(q, **dev) for q, dev in cases]
+    need = rq.srftq_prefix_attention_workspace(rq.make_desc(d, 2, 16, 4), n_seq, 4, 300)
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device=DEV)   # whatever it holds
+    got = [rq.prefix_attention(q, **dev, workspace=ws) for _ in range(30) for q, dev in cases]
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
+    assert rq.srftq_check_device() == 0
+
+
+def test_two_streams_at_once():
+    """Calls on two streams at the same time, each with the workspace that the
+    call allocates for itself."""
+    import torch
+    rng = np.random.default_rng(21)
+    cases = [_attn_case(rng, 30, 2, 4, 128, 4, 16, 0, 500, _ragged(rng, 30, 90), 16, "bfloat16")[:2]
+             for _ in range(2)]
+    want = [rq.prefix_attention(q, **dev) for q, dev in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, (q, dev) in enumerate(cases):
+            got[i].append(rq.prefix_attention(q, **dev, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o, want[i])
+
+
+def test_captured_step():
+    """Tables, codes and attention of a step captured together and replayed with
+    other lengths and vectors in the same buffers, a padded batch among them."""
+    import torch
+    rng = np.random.default_rng(22)
+    H, g, d, page, n_seq, pages = 2, 4, 128, 16, 6, 200
+    i32 = dict(dtype=torch.int32, device=DEV)
+    signs = _t(np.where(rng.random((2, H, d)) < 0.5, -1, 1).astype(np.int8))
+    lam = torch.rand((2, H, d), device=DEV) + 0.5
+    table0 = torch.arange(n_seq * 12, **i32).view(n_seq, 12)
+
+    def buffers():
+        return dict(codes=torch.zeros((2, pages * page, H, d // 2), dtype=torch.uint8, device=DEV),
+                    scales=torch.zeros((2, pages * page, H, d // 16), dtype=torch.float16, device=DEV),
+                    table=torch.cat([table0, torch.full((n_seq, 8), -1, **i32)], 1).contiguous(),
+                    cached=torch.zeros(n_seq, **i32), new=torch.zeros(n_seq, **i32),
+                    free=torch.zeros(40, **i32),
+                    x=torch.zeros((2, 160, H, d), dtype=torch.float16, device=DEV),
+                    q=torch.zeros((n_seq, H * g, d), dtype=torch.bfloat16, device=DEV))
+
+    def step(b):
+        slots, lens, _, _ = rq.block_tables(b["cached"], b["new"], b["free"], b["table"], page, 160)
+        rq.quantize_paged(b["x"], signs, lam, slots, b["codes"], b["scales"])
+        return rq.prefix_attention(b["q"], b["codes"][0], b["scales"][0], signs[0], lam[0],
+                                   b["codes"][1], b["scales"][1], signs[1], lam[1], b["table"], lens,
+                                   page_size=page)
+
+    graphed, eager = buffers(), buffers()
+    step(graphed)                                # what the first call of a kernel sets up
+    for k, v in buffers().items():
+        graphed[k].copy_(v)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = step(graphed)
+    cached = np.array([192, 100, 7, 0, 191, 33])
+    for it in range(3):
+        new = np.array([[9, 0, 40, 16, 1, 3], [1, 1, 1, 0, 1, 1], [0, 20, 0, 0, 5, 0]][it])
+        feed = dict(cached=_t(cached.astype(np.int32)), new=_t(new.astype(np.int32)),
+                    free=torch.arange(n_seq * 12 + 40 * it, n_seq * 12 + 40 * it + 40, **i32),
+                    x=_t(rng.standard_normal((2, 160, H, d)).astype(np.float16)),
+                    q=_t(rng.standard_normal((n_seq, H * g, d)).astype(np.float32)).bfloat16())
+        for b in (graphed, eager):
+            for k, v in feed.items():
+                b[k].copy_(v)
+        gr.replay()
+        want = step(eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(graphed["table"], eager["table"])
+        assert torch.equal(graphed["codes"], eager["codes"])
+        cached = cached + new
+    assert rq.srftq_check_device() == 0
 
 
 def test_serving_loop():
