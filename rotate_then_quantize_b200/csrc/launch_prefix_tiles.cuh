@@ -36,8 +36,8 @@ template <int D, int BITS, int G, bool EXACT>
 int launch_prefix_mma(const PrefixArgs& a, cudaStream_t stream) {
   const int64_t M = int64_t(a.n_seq) * a.q_per_kv;
   if constexpr (D == 256) {
-    using L = PrefixMma<D, BITS, G, EXACT>;
-    constexpr auto K = prefix_mma_kernel<D, BITS, G, EXACT>;
+    using L = PrefixMma<BITS, G, EXACT>;
+    constexpr auto K = prefix_mma_kernel<BITS, G, EXACT>;
     const int rc = prepare_smem<K>(L::kSmem);
     if (rc != SRFTQ_OK) return rc;
     const int64_t tiles = (M + kMmaRows - 1) / kMmaRows;

@@ -28,6 +28,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+
 #include "pages.cuh"
 #include "ptx.cuh"
 #include "warp_rotate.cuh"
@@ -35,7 +37,6 @@
 namespace srftq {
 
 constexpr int kPrefixRows = 8;        // query rows of one item
-constexpr int kPrefixMaxG = 16;       // query heads per KV head
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Plan of the own tokens, in the workspace: header, then start[n_seq + 1], the
@@ -314,6 +315,10 @@ __device__ __forceinline__ void ldmatrix_bytes_trans(uint32_t& r0, uint32_t& r1,
   asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0, %1}, [%2];"
                : "=r"(r0), "=r"(r1)
                : "r"(addr));
+}
+// 0x8000 in each half that is an infinite or NaN fp16.
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t s) {
+  return ((s & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -607,6 +612,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     float O[S16][4];
     // per column the reference of the weights (within 2^8 of the maximum), their sum
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int bad = INT_MAX;   // the first prefix token whose scale of values is not finite
 #pragma unroll
     for (int s = 0; s < S16; ++s)
 #pragma unroll
@@ -622,6 +628,29 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
       __syncwarp();
       const uint32_t st = ws_a + uint32_t(c % NS) * L::kStage;
       const int tk = p.t0 + kTileChunk * (warp + NW * c);
+
+      // A row that ends before a token has weight 0 there, which a scale that is not
+      // finite would still make NaN: such scales enter as 0, and the rows that reach
+      // the first of them take NaN for their sum at the end. (A sequence's own tokens
+      // end for all rows together, behind them are zeros.)
+      if (p.pre) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < (NG + 7) / 8; ++i) {
+          const uint4 u = lds128(st + L::kVS + lane * L::SBS + 16 * i);
+          any |= nonfinite_halves(u.x) | nonfinite_halves(u.y) | nonfinite_halves(u.z) |
+                 nonfinite_halves(u.w);
+        }
+        if (__any_sync(0xffffffffu, any != 0)) {
+          if (any) {
+            bad = min(bad, tk + lane);
+            uint16_t* sv = reinterpret_cast<uint16_t*>(ws + (c % NS) * L::kStage + L::kVS +
+                                                       lane * L::SBS);
+            for (int i = 0; i < NG; ++i) sv[i] = 0;
+          }
+          __syncwarp();
+        }
+      }
 
       // scores of the chunk's two tiles: rows g, g + 8 = tokens 2g, 2g + 1
       float S[2][4];
@@ -807,6 +836,12 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     for (int o = 4; o < 32; o <<= 1) {
       l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
       l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
+    }
+    if (p.pre) {
+      bad = __reduce_min_sync(0xffffffffu, bad);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (lim[c] > bad) l[c] = NAN;
     }
     if (g == 0) {
       ml_sh[warp][2 * t] = make_float2(m[0], l[0] * 0x1p-7f);

@@ -1,5 +1,5 @@
-// Parts of the shared prefix on the 5th-generation tensor cores (tcgen05), for
-// batches with many query rows per KV head.
+// The decoding of packed codes into fp16 tiles for tcgen05, and the parts of the
+// shared prefix for d = 256, for batches with many query rows per KV head.
 //
 // A block takes 128 query rows (of all sequences) of one head and a range of
 // the prefix's tokens, TN at a time:
@@ -21,9 +21,17 @@
 // rounding is that of the values, half a step of fp16, like the output's own.
 // For bf16 outputs, with steps 8 times as wide, one product each is enough.
 //
-// What bounds it: per 128 rows and 64 tokens at d = 128 the two products take
-// 512 clocks of the tensor cores and the exponentials 512 of the special
-// function units; two blocks per SM overlap them with the decoding.
+// One such unit fills an SM at d = 256: the queries (64 KB, 128 KB with their
+// rests) and two stages of keys and values leave no shared memory, O and two
+// score buffers no tensor memory for a second. For d = 64 and 128, where two
+// units fit, prefix_pair.cuh puts them into one block that decodes each tile
+// once for both.
+//
+// What bounds it: per 128 rows and 64 tokens the two products take 1024 clocks
+// of the tensor cores and the exponentials 512 of the special function units;
+// the decoding, by four warps, is next to them and not hidden behind another
+// unit's products. Against the warp-level kernel (8 rows at a time), a prefix of
+// 4096 tokens, 32 sequences x 8 queries per KV head: see kMmaMinRows.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -33,9 +41,10 @@ namespace srftq {
 
 constexpr int kMmaRows = 128;
 
-template <int D, int BITS, int G, bool EXACT>
+template <int BITS, int G, bool EXACT>
 struct PrefixMma {
-  static constexpr int TN = D == 256 && EXACT ? 32 : 64;      // tokens per step
+  static constexpr int D = 256;
+  static constexpr int TN = EXACT ? 32 : 64;                  // tokens per step
   static constexpr int CB = D * BITS / 8, NG = D / G;
   static constexpr int kPieces = D / 64;                      // 128-byte columns of a row
   static constexpr int kQPiece = kMmaRows * 128, kQ = kPieces * kQPiece;
@@ -51,11 +60,8 @@ struct PrefixMma {
   static constexpr int kSmem = kBytes + 1024;                 // slack to start on 1024 bytes
   static constexpr int kThreads = 288;
   static constexpr int kSCols = TN;                           // a score buffer
-  static constexpr int kOCol = 2 * TN < 64 ? 64 : 2 * TN;
-  static constexpr int kTmemCols = kOCol + D <= 128 ? 128 : kOCol + D <= 256 ? 256 : 512;
-  // blocks per SM: shared memory and tensor memory both allow them
-  static constexpr int kBlocks =
-      2 * (kSmem + 1024) <= 227 * 1024 && 2 * kTmemCols <= 512 ? 2 : 1;
+  static constexpr int kOCol = 2 * TN;
+  static constexpr int kTmemCols = 512;                       // a power of two >= kOCol + D
   static constexpr uint32_t kIdescS = f16_idesc<128, TN>();
   static constexpr uint32_t kIdescO = f16_idesc<128, D>() | (1u << 16);   // B is MN-major
 };
@@ -152,12 +158,33 @@ __device__ __forceinline__ void decode_pieces(uint32_t base, uint32_t rest_at, i
   }
 }
 
-template <int D, int BITS, int G, bool EXACT>
-__global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
-                                  PrefixMma<D, BITS, G, EXACT>::kBlocks)
+// Scales that are not finite may belong to tokens behind the end of some rows,
+// whose weights there are 0 and would still make NaN of them. So they enter the
+// products as 0, and the first token that has one goes to shared memory; the rows
+// that reach it take NaN for their sum at the end (each attends to all tokens
+// below its length, so the first is enough).
+template <int NK, class Tok>
+__device__ __forceinline__ void drop_nonfinite(uint32_t (&s)[NK], int* first_bad, Tok token) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < NK; ++k) any |= nonfinite_halves(s[k]);
+  if (any) {
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const uint32_t bad = nonfinite_halves(s[k]);
+      if (bad) {
+        s[k] &= ~((bad >> 15) * 0xFFFFu);
+        atomicMin(first_bad, token(k));
+      }
+    }
+  }
+}
+
+template <int BITS, int G, bool EXACT>
+__global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
     prefix_mma_kernel(const PrefixArgs a) {
-  using L = PrefixMma<D, BITS, G, EXACT>;
-  constexpr int TN = L::TN, CB = L::CB, NG = L::NG;   // tokens per step, code bytes, scales
+  using L = PrefixMma<BITS, G, EXACT>;
+  constexpr int D = L::D, TN = L::TN, CB = L::CB, NG = L::NG;   // tokens per step, code bytes, scales
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_a = smem_addr(smem_raw);
   uint8_t* smem = smem_raw + ((0u - raw_a) & 1023u);
@@ -169,6 +196,7 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
   uint64_t* qfull = bars + 14;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 16);
+  int* first_bad = reinterpret_cast<int*>(bars + 16) + 1;
   volatile uint8_t* on_sh = smem + L::kOnOff;
 
   // this block's head, rows and tokens
@@ -193,6 +221,7 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
     mbar_init(drain, 1);
     mbar_init(qfull, 1);
     *abort_flag = 0;
+    *first_bad = INT_MAX;
     fence_barrier_init();
   }
   if (warp == 8) {
@@ -322,6 +351,7 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
 #pragma unroll
         for (int k = 0; k < NK; ++k) on_sh[(i & 3) * TN + tr + k * RPP] = row[k] >= 0 ? 1 : 0;
       }
+      drop_nonfinite(ks, first_bad, [&](int k) { return token(i, k); });
       decode_pieces<D, BITS, G, TN, EXACT, NK>(sm + L::kKOff + st * L::kKT, L::kT, pc, tr, kw, ks, h_lo,
                                            h_hi);
       __threadfence_block();
@@ -332,6 +362,7 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
       if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&vempty[st], ((i >> 1) & 1) ^ 1,
                                                            abort_flag, a.guard)))
         break;
+      drop_nonfinite(vs, first_bad, [&](int k) { return token(i, k); });
       decode_pieces<D, BITS, G, TN, false, NK>(sm + L::kVOff + st * L::kT, 0, pc, tr, vw, vs, h_lo,
                                            h_hi);
       fence_proxy_async_smem();
@@ -453,6 +484,9 @@ __global__ void __launch_bounds__(PrefixMma<D, BITS, G, EXACT>::kThreads,
     // warp's looks at it here, and a parity cannot tell them apart.
     if (ok && __all_sync(0xffffffffu, wait_or_abort(drain, 0, abort_flag, a.guard))) {
       tc_fence_after();
+      // the decoders' last arrival, for what they have found
+      if (n > 0) (void)wait_or_abort(&vfull[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.guard);
+      if (lim > *first_bad) l = NAN;
       const int64_t part = (int64_t(part_i) * a.heads + h) * M + r0 + r;
       const bool live = r0 + r < M;
 #pragma unroll 1

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
   uint64_t* all_done = qfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(all_done + 2);
+  int* first_bad = reinterpret_cast<int*>(all_done + 2) + 1;
   volatile uint32_t* on_raw = reinterpret_cast<volatile uint32_t*>(smem + L::kOnOff);
   volatile uint32_t* on_ring = on_raw + 2 * NR;   // by tile, 16 of them
 
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
     for (int u = 0; u < 2; ++u) mbar_init(&qfull[u], 1);
     mbar_init(all_done, 2);
     *abort_flag = 0;
+    *first_bad = INT_MAX;
     fence_barrier_init();
   }
   if (warp == 16) {
@@ -317,6 +319,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
           s[k] = x;
         }
       }
+      drop_nonfinite(s, first_bad, [&](int k) { return t0 + j * TN + tr + k * RPP; });
       // an entry of the ring is written again 16 tiles on, long after the
       // softmax of this tile: at most the slots' tiles lie between
       if (tid == 256) {
@@ -442,6 +445,13 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
       }
       if (ok && __all_sync(0xffffffffu, wait_or_abort(all_done, 0, abort_flag, a.guard))) {
         tc_fence_after();
+        // the decoders' last arrivals, for what they have found
+        if (n > 0) {
+          const int sl = (n - 1) % NS, ph = ((n - 1) / NS) & 1;
+          (void)wait_or_abort(&kfull[sl], ph, abort_flag, a.guard);
+          (void)wait_or_abort(&vfull[sl], ph, abort_flag, a.guard);
+        }
+        if (lim > *first_bad) l = NAN;
         const int64_t part = (int64_t(SHARED ? part_i : 2 * part_i + u) * a.heads + h) * M + r0 + r;
         const bool live = r0 + r < M;
 #pragma unroll 1

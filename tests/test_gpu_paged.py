@@ -337,6 +337,35 @@ def test_prefix_attention_bad_pages():
     _check(q, dev, host)
 
 
+@pytest.mark.parametrize("d,bits,dtype,g", [
+    (128, 4, "float16", 2), (64, 8, "bfloat16", 1),      # few query rows
+    (128, 4, "float16", 8), (128, 8, "float16", 8), (64, 4, "bfloat16", 6),   # up to 128 rows
+    (128, 4, "bfloat16", 16), (64, 8, "bfloat16", 12),   # two row tiles
+    (256, 4, "float16", 4), (256, 8, "bfloat16", 6)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_prefix_attention_non_finite_prefix_token(d, bits, dtype, g, what):
+    """Scales of prefix tokens that are NaN or infinite reach the sequences that
+    attend to them and no other, though all share the tiles they lie in: of those
+    that end before, every bit is as without."""
+    rng = np.random.default_rng(d + bits + g)
+    n_seq, prefix = 14, 400
+    own = [3, -1 - 200, -1 - 203, 0, -1 - 64, -1 - 5, 60, -1 - 201, -1, -1 - 399, -1 - 399, 1, 2,
+           -1 - 202]
+    q, dev, host = _attn_case(rng, n_seq, 2, g, d, bits, 16, 0, prefix, own, 16, dtype)
+    want = rq.prefix_attention(q, **dev)
+    row = lambda t: int(paged.rows_of(host["prefix_table"], np.array([t]), 16, 10 ** 6)[0])
+    scales = dev[what + "_scales"]
+    scales[row(201), 1, 3] = float("nan")        # head 1 only
+    scales[row(250), 1, 0] = float("inf")
+    scales[row(399), 1] = float("-inf")
+    got = rq.prefix_attention(q, **dev)
+    assert rq.srftq_check_device() == 0
+    hit = _t(np.asarray(host["seq_lens"]) > 201)
+    assert bool((got[:, :g] == want[:, :g]).all())          # head 0
+    assert bool((got[~hit] == want[~hit]).all())
+    assert not bool(got[hit][:, g:].isfinite().any())
+
+
 def test_prefix_attention_all_pages_bad():
     """No token of a sequence has a page: zeros and -inf, as without tokens."""
     rng = np.random.default_rng(14)
