@@ -40,7 +40,8 @@
  * state. Calls enqueue work on `stream` (a cudaStream_t; NULL = legacy
  * default stream) and return without synchronising: SRFTQ_OK means
  * "launched". A call with zero vectors launches nothing. Every other
- * successful call launches exactly one kernel, the attention calls three.
+ * successful call launches exactly one kernel, but for the attention calls:
+ * srftq_decode_attention three, srftq_prefix_attention three or four.
  *
  * Errors: argument errors are detected on the host before anything is
  * launched and return a negative status. A launch failure returns
@@ -377,7 +378,9 @@ int srftq_dequantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_r
  * A sequence without tokens (len_b = 0, a padding row of the batch) gives
  * zeros. A sequence may be shorter than the prefix. A token whose table entry
  * is no page of the pool (negative, n_pages or more) is left out. What lies in
- * the pool behind a sequence's last token is never used, whatever it holds.
+ * the pool behind a sequence's last token is never used, whatever it holds; a
+ * scale that is not finite reaches the sequences that attend to its token only,
+ * among the shared tokens too.
  *
  *   q            [n_seq][heads*q_per_kv][d], out alike: fp16 or bf16 (dtype)
  *   k_codes, v_codes, k_scales, v_scales: pools of n_pages*page_size rows
@@ -391,8 +394,9 @@ int srftq_dequantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_r
  *                one each. Nothing in it is kept from one call to the next.
  *
  * The parts' softmax states are kept in float32 and joined in a fixed order:
- * the result does not depend on scheduling. Three launches, no copy to the
- * host: lengths and tables may come from calls before it on the stream.
+ * the result does not depend on scheduling. Three launches, four with many
+ * query rows per KV head, no copy to the host: lengths and tables may come from
+ * calls before it on the stream.
  */
 int srftq_prefix_attention(const srftq_desc* desc, int32_t dtype, int64_t n_seq, int32_t q_per_kv,
                            const void* q, const uint8_t* k_codes, const uint16_t* k_scales,

@@ -6,9 +6,20 @@
 
 namespace srftq {
 
-// Query rows per KV head from which the prefix goes to the tcgen05 kernel: it
-// computes 128 rows whatever their number, the other kernel 8 at a time.
-constexpr int64_t kMmaMinRows = 24, kMmaMinRowsExact = 40;
+// Which kernel takes the prefix. The tcgen05 kernels compute 128 query rows per
+// KV head whatever their number, the warp-level one 8 at a time, so its time per
+// token grows with the rows and breaks even at kEvenRows of each 128; a launch
+// more, the query tiles and a block's start cost the others 5 us, which the rows
+// beyond must win back over all tokens and heads. One B200, int4, fp16 / bf16, us
+// a call, warp-level against tcgen05:
+//   28672 tokens, 8 heads of d = 128: 16 rows 49 : 55 / 44 : 46, 24 rows 63 : 55 /
+//     53 : 46, 32 rows 75 : 55 / 65 : 45, 64 rows 126 : 59 / 110 : 49;
+//   28672 tokens, 4 heads of d = 256: 24 rows 69 : 104 / 61 : 69, 32 rows 83 : 103 /
+//     73 : 68, 48 rows 108 : 104 / 92 : 69;
+//   6000 tokens, d = 128: 24 rows 32 : 36 / 29 : 32, 32 rows 36 : 36 / 33 : 31;
+//   1024 tokens, d = 128: 32 rows 25 : 30 / 25 : 28, 48 rows 27 : 31 / 26 : 29.
+constexpr int64_t kMmaGain = 3 << 18;   // (rows beyond) x tokens x heads
+constexpr int64_t even_rows(int32_t d, bool exact) { return d <= 128 ? 16 : exact ? 46 : 30; }
 
 extern template int launch_prefix_tiles<64>(const PrefixArgs&, int, int, cudaStream_t);
 extern template int launch_prefix_tiles<128>(const PrefixArgs&, int, int, cudaStream_t);
@@ -21,7 +32,8 @@ namespace {
 struct PrefixShape {
   bool mma, shared;   // parts by tcgen05; its two units different rows, not alternate tokens
   int32_t splits, per, chunk_goal;
-  int64_t q_off, image_off, factor_off, plan_off, start_off, chunk_off, pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
+  int64_t q_off, image_off, factor_off, plan_off, start_off, chunk_off;
+  int64_t pre_ml_off, pre_acc_off, own_ml_off, own_acc_off, bytes;
 };
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
@@ -30,7 +42,8 @@ PrefixShape prefix_shape(int32_t d, int32_t heads, int64_t n_seq, int32_t g, int
                          bool exact, int sms) {
   PrefixShape s{};
   const int64_t rows = n_seq * g;
-  s.mma = prefix_len > 0 && rows >= (exact ? kMmaMinRowsExact : kMmaMinRows);
+  const int64_t even = (rows + kMmaRows - 1) / kMmaRows * even_rows(d, exact);
+  s.mma = rows > even && prefix_len > kMmaGain / (rows - even) / heads;
   if (prefix_len > 0) {
     // blocks of one wave, their row tiles, and what a block's start and end and
     // a part's join cost in tokens; the number of parts with the least time on

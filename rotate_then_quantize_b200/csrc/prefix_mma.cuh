@@ -30,8 +30,8 @@
 // What bounds it: per 128 rows and 64 tokens the two products take 1024 clocks
 // of the tensor cores and the exponentials 512 of the special function units;
 // the decoding, by four warps, is next to them and not hidden behind another
-// unit's products. Against the warp-level kernel (8 rows at a time), a prefix of
-// 4096 tokens, 32 sequences x 8 queries per KV head: see kMmaMinRows.
+// unit's products: 28672 tokens, 4 heads, up to 128 rows 69 us a call with bf16
+// outputs, 104 with fp16 (twice the products, and 32 tokens at a time).
 #pragma once
 
 #include "paged_attention.cuh"

@@ -16,10 +16,11 @@
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, a query row per thread. Warps
 // 8-11 and 12-15: codes of keys and of values to fp16 tiles (swizzled, sigma c /
 // 128 rounded once: at most |sigma|, so it cannot overflow). Warps 16 and 17:
-// issue the units' products. Warps 18 and 19: copy codes and scales of one tile each in turn into a ring of
-// raw stages, so that memory latency is hidden by depth, not by registers. O is rescaled only
-// when a row's maximum grows by more than 2^8 over the reference its weights use
-// (the weights stay below 2^15; the final quotient does not see the reference).
+// issue the units' products. Warps 18 and 19: copy codes and scales of a tile
+// each in turn into a ring of raw stages, so that memory latency is hidden by
+// depth, not by registers. O is rescaled only when a row's maximum grows by more
+// than 2^8 over the reference its weights use (the weights stay below 2^15; the
+// final quotient does not see the reference).
 //
 // The query row is scaled by a power of two to [2^13, 2^14) and rounded to
 // fp16. For fp16 outputs (EXACT) queries, keys and weights are split into an
@@ -29,7 +30,14 @@
 // wide, one product each is enough.
 //
 // What bounds it: 128 rows x 64 tokens are 512 clocks of the special function
-// units and, at d = 128, 512 of the tensor cores.
+// units and, at d = 128, 512 of the tensor cores; two units could keep both busy.
+// What it reaches is the chain of a tile: decode, scores, exponentials, values,
+// each handed on through a barrier. 128 sequences x 8 queries x 8 heads of d = 128
+// over 32768 int4 tokens, bf16: 168 us, against 80 of the products at the measured
+// dense rate. 16 x 8 x 8 over 131072 int8 tokens: 138 us the whole call, 39 of
+// products, 47 of memory; without the decoding of the two int8 tiles it took 43
+// less. On a small case ncu shows 28 % of the tensor pipe, 29 % of the special
+// function units and 36 % of the issue slots.
 #pragma once
 
 #include "prefix_mma.cuh"

@@ -245,6 +245,9 @@ SHAPES = [   # n_seq, H, g, prefix, most own, page
     (1, 1, 1, 0, 1, 16), (1, 2, 1, 1, 0, 16), (3, 2, 2, 37, 5, 16), (2, 1, 8, 0, 129, 1),
     (5, 3, 6, 100, 70, 24), (4, 2, 16, 64, 64, 64), (17, 1, 4, 129, 33, 32), (40, 2, 7, 300, 20, 16),
     (33, 1, 8, 1000, 3, 128), (3, 1, 3, 513, 300, 7), (130, 1, 2, 65, 9, 16),
+    # many rows and tokens, for the tcgen05 kernels: one row tile, a full one, three
+    (12, 4, 8, 4001, 20, 7), (16, 3, 8, 3203, 5, 1), (40, 2, 7, 3001, 20, 16),
+    (33, 1, 8, 6500, 3, 128),
 ]
 
 
@@ -275,7 +278,8 @@ def test_prefix_attention_peaked(n_seq, g):
     plus the output's own rounding, half a step."""
     import torch
     rng = np.random.default_rng(n_seq)
-    q, dev, host = _attn_case(rng, n_seq, 2, g, 128, 4, 16, 0, 700, _ragged(rng, n_seq, 100), 16,
+    q, dev, host = _attn_case(rng, n_seq, 2, g, 128, 4, 16, 0, 700 if n_seq == 2 else 3000,
+                              _ragged(rng, n_seq, 100), 16,
                               "bfloat16", q_gain=5.0)
     out = rq.prefix_attention(q, **dev).double().cpu().numpy()
     sd = np.zeros((*q.shape[:2], 1))
@@ -290,9 +294,10 @@ def test_prefix_attention_ignores_what_lies_behind():
     infinite scales, page numbers far outside the pool."""
     import torch
     rng = np.random.default_rng(12)
-    n_seq, prefix, page = 6, 70, 32
+    n_seq, page = 6, 32
     own = [5, 0, -1, 33, 1, 64]
-    for dtype, n_more in (("float16", 1), ("bfloat16", 40)):
+    for dtype, n_more, prefix in (("float16", 1, 70), ("bfloat16", 40, 70), ("bfloat16", 40, 1254),
+                                  ("float16", 20, 1254)):
         case = _attn_case(rng, n_seq * n_more, 2, 4, 128, 4, 16, 0, prefix, own * n_more, page,
                           dtype)
         q, dev, host = case
@@ -339,17 +344,17 @@ def test_prefix_attention_bad_pages():
 
 @pytest.mark.parametrize("d,bits,dtype,g", [
     (128, 4, "float16", 2), (64, 8, "bfloat16", 1),      # few query rows
-    (128, 4, "float16", 8), (128, 8, "float16", 8), (64, 4, "bfloat16", 6),   # up to 128 rows
+    (128, 4, "float16", 8), (128, 8, "float16", 8), (64, 4, "bfloat16", 8),   # up to 128 rows
     (128, 4, "bfloat16", 16), (64, 8, "bfloat16", 12),   # two row tiles
-    (256, 4, "float16", 4), (256, 8, "bfloat16", 6)])
+    (256, 4, "float16", 16), (256, 8, "bfloat16", 12), (256, 4, "bfloat16", 1)])
 @pytest.mark.parametrize("what", ["k", "v"])
 def test_prefix_attention_non_finite_prefix_token(d, bits, dtype, g, what):
     """Scales of prefix tokens that are NaN or infinite reach the sequences that
     attend to them and no other, though all share the tiles they lie in: of those
     that end before, every bit is as without."""
     rng = np.random.default_rng(d + bits + g)
-    n_seq, prefix = 14, 400
-    own = [3, -1 - 200, -1 - 203, 0, -1 - 64, -1 - 5, 60, -1 - 201, -1, -1 - 399, -1 - 399, 1, 2,
+    n_seq, prefix = 14, 4800
+    own = [3, -1 - 200, -1 - 203, 0, -1 - 64, -1 - 5, 60, -1 - 201, -1, -1 - 4799, -1 - 4799, 1, 2,
            -1 - 202]
     q, dev, host = _attn_case(rng, n_seq, 2, g, d, bits, 16, 0, prefix, own, 16, dtype)
     want = rq.prefix_attention(q, **dev)
@@ -357,7 +362,7 @@ def test_prefix_attention_non_finite_prefix_token(d, bits, dtype, g, what):
     scales = dev[what + "_scales"]
     scales[row(201), 1, 3] = float("nan")        # head 1 only
     scales[row(250), 1, 0] = float("inf")
-    scales[row(399), 1] = float("-inf")
+    scales[row(4799), 1] = float("-inf")
     got = rq.prefix_attention(q, **dev)
     assert rq.srftq_check_device() == 0
     hit = _t(np.asarray(host["seq_lens"]) > 201)
@@ -376,11 +381,12 @@ def test_prefix_attention_all_pages_bad():
     assert (out == 0).all() and (lse == -math.inf).all()
 
 
-def test_prefix_attention_non_finite_query():
+@pytest.mark.parametrize("prefix", [200, 7000])
+def test_prefix_attention_non_finite_query(prefix):
     """A NaN in one query stays in that query's output."""
     import torch
     rng = np.random.default_rng(15)
-    q, dev, host = _attn_case(rng, 40, 1, 4, 128, 4, 16, 0, 200, _ragged(rng, 40, 30), 16,
+    q, dev, host = _attn_case(rng, 40, 1, 4, 128, 4, 16, 0, prefix, _ragged(rng, 40, 30), 16,
                               "float16")
     want = rq.prefix_attention(q, **dev)
     q2 = q.clone()
@@ -429,12 +435,13 @@ def test_prefix_attention_far_rows():
 # Streams, graphs and the run of all three
 # ---------------------------------------------------------------------------
 
-def test_other_stream_and_graphs():
+@pytest.mark.parametrize("prefix", [130, 50_003])
+def test_other_stream_and_graphs(prefix):
     """A call on another stream, and two captured graphs with a workspace each,
     replayed with new lengths and queries in the same buffers."""
     import torch
     rng = np.random.default_rng(18)
-    q, dev, host = _attn_case(rng, 6, 2, 4, 128, 4, 16, 0, 130, [60, 9, 0, 33, 1, 64], 16,
+    q, dev, host = _attn_case(rng, 6, 2, 4, 128, 4, 16, 0, prefix, [60, 9, 0, 33, 1, 64], 16,
                               "float16")
     want = rq.prefix_attention(q, **dev)
     side = torch.cuda.Stream()
@@ -443,7 +450,7 @@ def test_other_stream_and_graphs():
     side.synchronize()
     assert torch.equal(got, want)
     desc = rq.make_desc(128, 2, 16, 4)
-    ws = [torch.empty(rq.srftq_prefix_attention_workspace(desc, 6, 4, 130), dtype=torch.uint8,
+    ws = [torch.empty(rq.srftq_prefix_attention_workspace(desc, 6, 4, prefix), dtype=torch.uint8,
                       device=DEV) for _ in range(2)]
     outs = [torch.empty_like(q) for _ in range(2)]
     graphs = []
@@ -462,17 +469,18 @@ def test_other_stream_and_graphs():
         assert torch.equal(o, want.flip(0))
 
 
-@pytest.mark.parametrize("dtype,n_seq,d", [("bfloat16", 40, 128), ("float16", 20, 64),
-                                           ("float16", 3, 128), ("bfloat16", 12, 256)])
-def test_one_workspace_for_calls_in_turn(dtype, n_seq, d):
+@pytest.mark.parametrize("dtype,n_seq,d,prefix", [
+    ("bfloat16", 40, 128, 6600), ("float16", 20, 64, 6600), ("float16", 3, 128, 300),
+    ("bfloat16", 24, 256, 6600), ("bfloat16", 40, 64, 300)])
+def test_one_workspace_for_calls_in_turn(dtype, n_seq, d, prefix):
     """Calls in a stream may share a workspace: two batches in turn, thirty
     times without a wait between, with the results they have by themselves."""
     import torch
     rng = np.random.default_rng(20)
-    cases = [_attn_case(rng, n_seq, 2, 4, d, 4, 16, 0, 300, _ragged(rng, n_seq, 200 - 150 * i), 16,
-                        dtype)[:2] for i in range(2)]
+    cases = [_attn_case(rng, n_seq, 2, 4, d, 4, 16, 0, prefix,
+                        _ragged(rng, n_seq, 200 - 150 * i), 16, dtype)[:2] for i in range(2)]
     want = [rq.prefix_attention(q, **dev) for q, dev in cases]
-    need = rq.srftq_prefix_attention_workspace(rq.make_desc(d, 2, 16, 4), n_seq, 4, 300)
+    need = rq.srftq_prefix_attention_workspace(rq.make_desc(d, 2, 16, 4), n_seq, 4, prefix)
     ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device=DEV)   # whatever it holds
     got = [rq.prefix_attention(q, **dev, workspace=ws) for _ in range(30) for q, dev in cases]
     for i, o in enumerate(got):
@@ -485,7 +493,7 @@ def test_two_streams_at_once():
     call allocates for itself."""
     import torch
     rng = np.random.default_rng(21)
-    cases = [_attn_case(rng, 30, 2, 4, 128, 4, 16, 0, 500, _ragged(rng, 30, 90), 16, "bfloat16")[:2]
+    cases = [_attn_case(rng, 30, 2, 4, 128, 4, 16, 0, 4000, _ragged(rng, 30, 90), 16, "bfloat16")[:2]
              for _ in range(2)]
     want = [rq.prefix_attention(q, **dev) for q, dev in cases]
     torch.cuda.synchronize()
