@@ -176,8 +176,7 @@ __device__ __forceinline__ int query_exponent(float amax) {
 // memory as they are: tiles of 128 rows, each (for fp16 outputs) followed by the
 // rests; a tile is d / 64 pieces of rows of 128 bytes whose 16-byte chunks are
 // XOR-swizzled by the row. The 8 coordinates of a chunk lie in the order that
-// decoding the codes gives (prefix_mma.cuh: decoded_coord), odd ones over 16 for
-// int4, whose odd codes come out 16 times too large.
+// decoding the codes gives (prefix_mma.cuh: decoded_coord).
 template <int D>
 struct QueryRow {
   uint8_t* p;
@@ -196,7 +195,6 @@ struct QueryRow {
   __device__ __forceinline__ void put(int c, float x) const {
     const int at = four ? (c & 3) * 2 + ((c >> 2) & 1)
                         : (c & 4) + (c & 1) * 2 + ((c >> 1) & 1);
-    if (four && (c & 1)) x *= 0.0625f;
     uint8_t* q = p + (c >> 6) * 16384 + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + at * 2;
     const __half hi = __float2half_rn(x);
     *reinterpret_cast<__half*>(q) = hi;
@@ -250,7 +248,7 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
         row.put(2 * k, z[e].x * up);
         row.put(2 * k + 1, z[e].y * up);
       }
-      if (lane == 0) *row.factor = __uint_as_float(uint32_t(127 - e2) << 23) * 128.0f;
+      if (lane == 0) *row.factor = __uint_as_float(uint32_t(127 - e2) << 23) * (a.bits == 4 ? 8.0f : 128.0f);
     }
   }
   if (a.pre_mma) {   // rows behind the last query: zeros
@@ -283,10 +281,12 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
 // only rounding to fewer bits is the query's: 2^-12 for bf16 outputs (whose own
 // step is 2^-9), 2^-23 for fp16.
 //
-// Values, O[coord][query] += sum_t (sigma c / 128)[coord][t] p'[t][query], p' =
+// Values, O[coord][query] += sum_t (sigma c / C)[coord][t] p'[t][query], C = 8
+// (int4) or 128 (int8), p' =
 // 2^7 e^{x - m}, m a reference that follows the maximum when that grows by more
-// than 2^8 (the factors keep small weights normal and large ones below 2^15). sigma c / 128 is
-// rounded once to fp16: at most |sigma|, so it never overflows. The 8-bit
+// than 2^8 (the factors keep small weights normal and large ones below 2^15). sigma c / C is
+// rounded once to fp16: at most |sigma|, so it never overflows, and no smaller
+// than that allows, so it keeps its bits while sigma is a normal number. The 8-bit
 // transposing ldmatrix gives lane (g, t) coordinate g of tokens 4t .. 4t + 3,
 // and the score rows take their tokens in the order that hands the lane's p'
 // over with one movmatrix. p' is fp16 hi (+ lo for fp16 outputs).
@@ -799,9 +799,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
           mma_f16(O[s], a0, a1, a2, a3, ph[mt][0], ph[mt][1]);
           if constexpr (EXACT) mma_f16(O[s], a0, a1, a2, a3, pl[mt][0], pl[mt][1]);
         };
-        // fp16 1024 + u, or 1024 + 16 u, to c / 128 or 16 c / 128 (exact)
-        constexpr uint32_t k128 = 0x20002000u;                       // 2^-7
-        constexpr uint32_t o8 = 0xC808C808u, o128 = 0xC880C880u;     // -1032 / 128, -1152 / 128
+        // fp16 1024 + u, or 1024 + 16 u, to c / 8 (int4) or c / 128 (exact)
+        constexpr uint32_t k8 = 0x30003000u, k128 = 0x20002000u;     // 2^-3, 2^-7
+        constexpr uint32_t o8 = 0xD808D808u, o128 = 0xC880C880u;     // -1032 / 8, -1152 / 128
         if constexpr (BITS == 4) {
 #pragma unroll
           for (int s = 0; s < S16; s += 2) {
@@ -810,9 +810,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t y = r[i] >> 8;
-              weigh(s + i, hfma2((r[i] & 0x000F000Fu) ^ h_lo, k128, o8),
+              weigh(s + i, hfma2((r[i] & 0x000F000Fu) ^ h_lo, k8, o8),
                     hfma2((r[i] & 0x00F000F0u) ^ h_hi, k128, o128),
-                    hfma2((y & 0x000F000Fu) ^ h_lo, k128, o8),
+                    hfma2((y & 0x000F000Fu) ^ h_lo, k8, o8),
                     hfma2((y & 0x00F000F0u) ^ h_hi, k128, o128));
             }
           }
@@ -852,17 +852,17 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     }
 #pragma unroll
     for (int s = 0; s < S16; ++s) {
-      constexpr float f0 = 1.0f, f1 = BITS == 4 ? 0.0625f : 1.0f;   // 128 / 2^7 (/ 16)
+      constexpr float f = BITS == 4 ? 0.0625f : 1.0f;   // C / 2^7
       if constexpr (BITS == 4) {   // rows g, g + 8: coordinates 2g, 2g + 1
         float* o = wo + 2 * t * D + 16 * s + 2 * g;
-        *reinterpret_cast<float2*>(o) = make_float2(O[s][0] * f0, O[s][2] * f1);
-        *reinterpret_cast<float2*>(o + D) = make_float2(O[s][1] * f0, O[s][3] * f1);
+        *reinterpret_cast<float2*>(o) = make_float2(O[s][0] * f, O[s][2] * f);
+        *reinterpret_cast<float2*>(o + D) = make_float2(O[s][1] * f, O[s][3] * f);
       } else {                     // coordinates g, g + 8
         float* o = wo + 2 * t * D + 16 * s + g;
-        o[0] = O[s][0] * f0;
-        o[8] = O[s][2] * f1;
-        o[D] = O[s][1] * f0;
-        o[D + 8] = O[s][3] * f1;
+        o[0] = O[s][0] * f;
+        o[8] = O[s][2] * f;
+        o[D] = O[s][1] * f;
+        o[D + 8] = O[s][3] * f;
       }
     }
     if (threadIdx.x == 0) {

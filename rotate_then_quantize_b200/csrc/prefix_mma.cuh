@@ -3,11 +3,13 @@
 //
 // A block takes 128 query rows (of all sequences) of one head and a range of
 // the prefix's tokens, TN at a time:
-//   S[row][token]  = Q (sigma c / 128)^T      both operands in shared memory;
+//   S[row][token]  = Q (sigma c / C)^T        both operands in shared memory,
+//                    C = 8 (int4) or 128 (int8);
 //   P[row][token]  = 2^7 e^{x - ref}, fp16, written over S in tensor memory;
-//   O[row][coord] += P (sigma c / 128)        P from tensor memory.
-// Warps 4-7 turn packed codes into swizzled fp16 tiles (sigma c / 128, rounded
-// once: at most |sigma|, so it cannot overflow), warp 8 issues the products,
+//   O[row][coord] += P (sigma c / C)          P from tensor memory.
+// Warps 4-7 turn packed codes into swizzled fp16 tiles (sigma c / C, rounded
+// once: at most |sigma|, so it cannot overflow, and no smaller than that
+// allows), warp 8 issues the products,
 // warps 0-3 hold a query row per thread: its maximum and sum need no exchange.
 // Two score buffers let the tensor cores form the next scores while the
 // exponentials of these are taken. O is rescaled only when a row's maximum
@@ -71,32 +73,32 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// What decoded codes are divided by, a power of two >= |c|.
+template <int BITS>
+constexpr float kCodeUnit = BITS == 4 ? 8.0f : 128.0f;
+
 // Position p of 8 consecutive coordinates in the decoded order: the code pairs
-// that one AND isolates. int4: (0, 4), 16 (1, 5), (2, 6), 16 (3, 7); int8, two
-// words of 4: (0, 2), (1, 3) each.
+// that one AND isolates. int4: (0, 4), (1, 5), (2, 6), (3, 7); int8, two words of
+// 4: (0, 2), (1, 3) each.
 template <int BITS>
 __host__ __device__ constexpr int decoded_coord(int p) {
   return BITS == 4 ? (p & 1) * 4 + (p >> 1) : (p & 4) + 2 * (p & 1) + ((p >> 1) & 1);
 }
-template <int BITS>
-__host__ __device__ constexpr bool decoded_times16(int p) {
-  return BITS == 4 && ((p >> 1) & 1);
-}
 
-// 8 codes (1 or 2 words) to sigma c / 128 in decoded order: v rounded to fp16,
+// 8 codes (1 or 2 words) to sigma c / kCodeUnit in decoded order: v rounded to fp16,
 // rest what that left (exact, but for subnormals). h_lo, h_hi: the magic numbers
 // 1024 + u and 1024 + 16 u in registers.
 template <int BITS, bool REST>
 __device__ __forceinline__ void decode_chunk(const uint32_t* w, uint32_t sg2, uint32_t h_lo,
                                              uint32_t h_hi, uint4& v, uint4& rest) {
-  constexpr uint32_t k128 = 0x20002000u;                     // 2^-7
-  constexpr uint32_t o8 = 0xC808C808u, o128 = 0xC880C880u;   // -1032 / 128, -1152 / 128
+  constexpr uint32_t k8 = 0x30003000u, k128 = 0x20002000u;   // 2^-3, 2^-7
+  constexpr uint32_t o8 = 0xD808D808u, o128 = 0xC880C880u;   // -1032 / 8, -1152 / 128
   uint32_t c[4];
   if constexpr (BITS == 4) {
     const uint32_t y = w[0] >> 8;
-    c[0] = hfma2((w[0] & 0x000F000Fu) ^ h_lo, k128, o8);
-    c[1] = hfma2((w[0] & 0x00F000F0u) ^ h_hi, k128, o128);
-    c[2] = hfma2((y & 0x000F000Fu) ^ h_lo, k128, o8);
+    c[0] = hfma2((w[0] & 0x000F000Fu) ^ h_lo, k8, o8);
+    c[1] = hfma2((w[0] & 0x00F000F0u) ^ h_hi, k128, o128);   // 16 c / 128
+    c[2] = hfma2((y & 0x000F000Fu) ^ h_lo, k8, o8);
     c[3] = hfma2((y & 0x00F000F0u) ^ h_hi, k128, o128);
   } else {
 #pragma unroll
@@ -497,9 +499,9 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
         if (live) {
           float y[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)   // 128 / 2^7 = 1
+          for (int j = 0; j < 32; ++j)
             y[(j & ~7) + decoded_coord<BITS>(j & 7)] =
-                __uint_as_float(o[j]) * (decoded_times16<BITS>(j & 7) ? 0.0625f : 1.0f);
+                __uint_as_float(o[j]) * (kCodeUnit<BITS> * 0x1p-7f);
           float4* dst = reinterpret_cast<float4*>(a.pre_acc + part * D + k);
 #pragma unroll
           for (int j = 0; j < 8; ++j)

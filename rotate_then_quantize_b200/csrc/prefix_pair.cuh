@@ -3,9 +3,10 @@
 //
 // A unit is 128 query rows with two score tiles S, the weights P written over
 // them, and an accumulator O, all in tensor memory:
-//   S[row][token]  = Q (sigma c / 128)^T      TN = 64 tokens at a time;
+//   S[row][token]  = Q (sigma c / C)^T        TN = 64 tokens at a time, C = 8
+//                    (int4) or 128 (int8);
 //   P[row][token]  = 2^7 e^{x - ref}, fp16, written over S;
-//   O[row][coord] += P (sigma c / 128).
+//   O[row][coord] += P (sigma c / C).
 // The scores of a unit's next tile are formed while its four warps take the
 // exponentials of this one. Two forms:
 //   shared   the units are 256 different rows over the same tokens: a token's
@@ -15,7 +16,7 @@
 //
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, a query row per thread. Warps
 // 8-11 and 12-15: codes of keys and of values to fp16 tiles (swizzled, sigma c /
-// 128 rounded once: at most |sigma|, so it cannot overflow). Warps 16 and 17:
+// C rounded once: at most |sigma|, so it cannot overflow). Warps 16 and 17:
 // issue the units' products. Warps 18 and 19: copy codes and scales of a tile
 // each in turn into a ring of raw stages, so that memory latency is hidden by
 // depth, not by registers. O is rescaled only when a row's maximum grows by more
@@ -475,9 +476,9 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
           if (live) {
             float y[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)   // 128 / 2^7 = 1
+            for (int i = 0; i < 32; ++i)
               y[(i & ~7) + decoded_coord<BITS>(i & 7)] =
-                  __uint_as_float(o[i]) * (decoded_times16<BITS>(i & 7) ? 0.0625f : 1.0f);
+                  __uint_as_float(o[i]) * (kCodeUnit<BITS> * 0x1p-7f);
             float4* dst = reinterpret_cast<float4*>(a.pre_acc + part * D + k);
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -371,6 +371,25 @@ def test_prefix_attention_non_finite_prefix_token(d, bits, dtype, g, what):
     assert not bool(got[hit][:, g:].isfinite().any())
 
 
+@pytest.mark.parametrize("n_seq,prefix,bits,d,dtype", [
+    (3, 100, 4, 128, "float16"), (3, 100, 8, 64, "float16"), (20, 6600, 4, 128, "float16"),
+    (50, 6600, 4, 64, "bfloat16"), (30, 6600, 4, 256, "float16"), (20, 6600, 8, 128, "float16")])
+def test_prefix_attention_small_scales(n_seq, prefix, bits, d, dtype):
+    """Scales 2^-9 (int8: 2^-5) of the usual ones, with lambda as much larger:
+    the same vectors, so the same result. The values keep their bits as long as
+    their scale is a normal number."""
+    rng = np.random.default_rng(n_seq + bits + d)
+    q, dev, host = _attn_case(rng, n_seq, 2, 4, d, bits, 16, 0, prefix, _ragged(rng, n_seq, 90), 16,
+                              dtype)
+    k = 9 if bits == 4 else 5
+    for c in "kv":
+        small = dev[c + "_scales"].float() * 2.0 ** -k
+        assert bool((small.half().float() == small).all())
+        dev[c + "_scales"] = small.half()
+        dev[c + "_lambda"] = dev[c + "_lambda"] * 2.0 ** k
+    _check(q, dev, host)
+
+
 def test_prefix_attention_all_pages_bad():
     """No token of a sequence has a page: zeros and -inf, as without tokens."""
     rng = np.random.default_rng(14)
