@@ -507,6 +507,31 @@ def test_one_workspace_for_calls_in_turn(dtype, n_seq, d, prefix):
     assert rq.srftq_check_device() == 0
 
 
+@pytest.mark.parametrize("prefix,n_seq", [(64, 6), (6400, 20)])
+def test_tokens_written_between_calls(prefix, n_seq):
+    """Tokens are written into pages between calls, in place beside ones that the
+    call before has read: as with copies of pools and tables at other addresses."""
+    import torch
+    rng = np.random.default_rng(23)
+    H, d, page = 2, 128, 16
+    q, dev, _ = _attn_case(rng, n_seq, H, 4, d, 4, 16, 0, prefix, [40] * n_seq, page, "bfloat16")
+    i32 = dict(dtype=torch.int32, device=DEV)
+    dev["seq_lens"] = torch.full((n_seq,), prefix + 20, **i32)
+    table = dev["block_table"].long()
+    b = torch.arange(n_seq, device=DEV)
+    for t in range(prefix + 20, prefix + 40):
+        slots = table[b, t // page] * page + t % page
+        for c in "kv":
+            x = torch.randn((1, n_seq, H, d), device=DEV).half()
+            rq.quantize_paged(x, dev[c + "_signs"][None], dev[c + "_lambda"][None], slots,
+                              dev[c + "_codes"][None], dev[c + "_scales"][None])
+        dev["seq_lens"] += 1
+        got = rq.prefix_attention(q, **dev)
+        fresh = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in dev.items()}
+        assert torch.equal(got, rq.prefix_attention(q, **fresh)), t
+    assert rq.srftq_check_device() == 0
+
+
 def test_two_streams_at_once():
     """Calls on two streams at the same time, each with the workspace that the
     call allocates for itself."""
