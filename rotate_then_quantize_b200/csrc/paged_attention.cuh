@@ -32,6 +32,7 @@
 
 #include "pages.cuh"
 #include "ptx.cuh"
+#include "token_plan.cuh"
 #include "warp_rotate.cuh"
 
 namespace srftq {
@@ -128,12 +129,11 @@ __device__ inline void plan_own_tokens(const PrefixArgs& a) {
   for (int w = 0; w < nt / 32; ++w) total += total_sh[w];
   // chunks of at least 128 tokens (a tile for each warp), few enough that
   // sum ceil(own / chunk) <= goal + n_seq
-  const int64_t per = (total + a.chunk_goal - 1) / a.chunk_goal;
-  const int32_t chunk = int32_t(per <= 128 ? 128 : (per + 127) / 128 * 128);
+  const int32_t chunk = chunk_tokens(total, a.chunk_goal);
   int32_t carry = 0;
   for (int b0 = 0; b0 < a.n_seq; b0 += nt) {
     const int b = b0 + tid;
-    const int32_t n = b < a.n_seq ? (a.own(b) + chunk - 1) / chunk : 0;
+    const int32_t n = b < a.n_seq ? chunks_of(a.own(b), chunk) : 0;
     int32_t v = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -153,10 +153,12 @@ __device__ inline void plan_own_tokens(const PrefixArgs& a) {
   }
   // the chunks' sequences and tokens, so that a block has its next item in one load
   for (int b = tid; b < a.n_seq; b += nt) {
-    const int32_t end = a.len(b), own = a.own(b);
+    const int32_t end = a.len(b), n = chunks_of(a.own(b), chunk);
     int4* o = a.chunk_of + a.chunk_start[b];   // this thread wrote it
-    for (int32_t c = 0; c * int64_t(chunk) < own; ++c)
-      o[c] = make_int4(b, a.prefix_len + c * chunk, min(a.prefix_len + (c + 1) * chunk, end), 0);
+    for (int32_t c = 0; c < n; ++c) {
+      const int32_t t0 = a.prefix_len + c * chunk;
+      o[c] = make_int4(b, t0, range_end(t0, chunk, end), 0);
+    }
   }
   if (tid == 0) {
     a.chunk_start[a.n_seq] = carry;
@@ -435,7 +437,7 @@ __device__ __forceinline__ PartItem pre_item(const PrefixArgs& a, int64_t i, int
   p.r0 = rt * kPrefixRows;
   p.nr = min(kPrefixRows, M - p.r0);
   p.t0 = s * a.prefix_per;
-  p.t1 = min(p.t0 + a.prefix_per, a.prefix_len);
+  p.t1 = range_end(p.t0, a.prefix_per, a.prefix_len);
   p.part = (int64_t(s) * a.heads + p.h) * M + p.r0;
   p.table = a.prefix_table;
   return p;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
   const int rt = int(blockIdx.x) % tiles, sh = int(blockIdx.x) / tiles;
   const int h = sh % a.heads, part_i = sh / a.heads;
   const int r0 = rt * kMmaRows;
-  const int t0 = part_i * a.prefix_per, t1 = min(t0 + a.prefix_per, a.prefix_len);
+  const int t0 = part_i * a.prefix_per, t1 = range_end(t0, a.prefix_per, a.prefix_len);
   const int n = (t1 - t0 + TN - 1) / TN;
 
   if (tid == 0) {

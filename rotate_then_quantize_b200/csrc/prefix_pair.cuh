@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
   const int blocks = (M + ROWS - 1) / ROWS, tiles = (M + kMmaRows - 1) / kMmaRows;
   const int rt = int(blockIdx.x) % blocks, sh = int(blockIdx.x) / blocks;
   const int h = sh % a.heads, part_i = sh / a.heads;
-  const int t0 = part_i * a.prefix_per, t1 = min(t0 + a.prefix_per, a.prefix_len);
+  const int t0 = part_i * a.prefix_per, t1 = range_end(t0, a.prefix_per, a.prefix_len);
   const int n = (t1 - t0 + TN - 1) / TN;                           // tiles of 64 tokens
   // units with rows: both, or (shared, an odd last tile of rows) the first
   const int units = SHARED && 2 * rt + 1 >= tiles ? 1 : 2;
