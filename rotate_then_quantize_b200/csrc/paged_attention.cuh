@@ -106,7 +106,11 @@ __device__ __forceinline__ float hi_f32(uint32_t w, bool bf16) {
 }
 
 // Programmatic launches (launch_after): the next grid may start from here on;
-// the grids before this one are complete from here on.
+// the grids before this one are complete from here on. So a grid may be resident
+// while the one before still writes the workspace: what it finds there it reads
+// with ordinary loads, never through the read-only path (__ldg), which may return
+// what a line held before. The caller's inputs are complete before the first
+// launch starts.
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;");
 }
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
   __shared__ int32_t next_sh;
   __shared__ int4 rec_sh;
   auto record = [&](int64_t i) {
-    return i >= n_pre && i < n_items ? __ldg(a.chunk_of + own_chunk(a, i - n_pre, own_tiles))
+    return i >= n_pre && i < n_items ? a.chunk_of[own_chunk(a, i - n_pre, own_tiles)]
                                      : make_int4(0, 0, 0, 0);
   };
   int4 rec = record(blockIdx.x);
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     float amax = 0.0f;
 #pragma unroll
     for (int s = 0; s < S16; ++s) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(qv + 16 * s + 4 * t));
+      const float4 x = *reinterpret_cast<const float4*>(qv + 16 * s + 4 * t);
       amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
 #pragma unroll
     for (int i = 0; i < S16 / NW; ++i) {
       const int s = warp + NW * i;
-      const float4 x = __ldg(reinterpret_cast<const float4*>(qv + 16 * s + 4 * t));
+      const float4 x = *reinterpret_cast<const float4*>(qv + 16 * s + 4 * t);
       constexpr float odd = BITS == 4 ? 0.0625f : 1.0f;   // int4: odd coordinates' codes are 16 u
       const float x0 = x.x * up, x1 = x.y * up * odd, x2 = x.z * up, x3 = x.w * up * odd;
       const uint2 hi = make_uint2(pack_half2(x0, x2), pack_half2(x1, x3));
