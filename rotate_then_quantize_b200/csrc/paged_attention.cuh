@@ -22,7 +22,9 @@
 //                           split of the sequences' own tokens;
 //   prefix_tile_kernel      the parts, each (m, l, a) into the workspace;
 //   prefix_merge_kernel     1, 4 or 16 warps per query head: joins its parts,
-//                           applies lambda_V / l, R_V^T and s_V, rounds once.
+//                           applies lambda_V / l, R_V^T and s_V, rounds once. A
+//                           head whose sums are not finite, for a scale too large
+//                           for the parts' fp16 (kLargeScale), is done anew there.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
         row.put(2 * k, z[e].x * up);
         row.put(2 * k + 1, z[e].y * up);
       }
-      if (lane == 0) *row.factor = __uint_as_float(uint32_t(127 - e2) << 23) * (a.bits == 4 ? 8.0f : 128.0f);
+      if (lane == 0) *row.factor = __uint_as_float(uint32_t(127 - e2) << 23);
     }
   }
   if (a.pre_mma) {   // rows behind the last query: zeros
@@ -287,12 +289,10 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
 // only rounding to fewer bits is the query's: 2^-12 for bf16 outputs (whose own
 // step is 2^-9), 2^-23 for fp16.
 //
-// Values, O[coord][query] += sum_t (sigma c / C)[coord][t] p'[t][query], C = 8
-// (int4) or 128 (int8), p' =
+// Values, O[coord][query] += sum_t (sigma c)[coord][t] p'[t][query], p' =
 // 2^7 e^{x - m}, m a reference that follows the maximum when that grows by more
-// than 2^8 (the factors keep small weights normal and large ones below 2^15). sigma c / C is
-// rounded once to fp16: at most |sigma|, so it never overflows, and no smaller
-// than that allows, so it keeps its bits while sigma is a normal number. The 8-bit
+// than 2^8 (the factors keep small weights normal and large ones below 2^15).
+// sigma c is rounded once to fp16 (kLargeScale). The 8-bit
 // transposing ldmatrix gives lane (g, t) coordinate g of tokens 4t .. 4t + 3,
 // and the score rows take their tokens in the order that hands the lane's p'
 // over with one movmatrix. p' is fp16 hi (+ lo for fp16 outputs).
@@ -325,9 +325,19 @@ __device__ __forceinline__ void ldmatrix_bytes_trans(uint32_t& r0, uint32_t& r1,
                : "=r"(r0), "=r"(r1)
                : "r"(addr));
 }
-// 0x8000 in each half that is an infinite or NaN fp16.
-__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t s) {
-  return ((s & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+// The products sigma c are held as fp16. A scale is a whole number of 2^-24 and c
+// a whole number, so sigma c has no bits below the subnormals' last one: it is
+// rounded to 11 significant bits and to nothing else, however small the scale.
+// Scales below this one, 8192 with |c| <= 8 or 512 with |c| <= 128, keep it at
+// 65504 at most. A row that attends to a token with a larger scale, or with one
+// that is not finite, takes NaN for its sum, and the join does it anew in float32.
+// Calibrated scales are of order one; only vectors next to fp16's own end reach it.
+template <int BITS>
+constexpr uint32_t kLargeScale = BITS == 4 ? 0x7000u : 0x6000u;
+// 0x8000 in each half whose magnitude is at least that, infinite or NaN.
+template <int BITS>
+__device__ __forceinline__ uint32_t large_halves(uint32_t s) {
+  return ((s & 0x7FFF7FFFu) + (0x8000u - kLargeScale<BITS>) * 0x10001u) & 0x80008000u;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -621,7 +631,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     float O[S16][4];
     // per column the reference of the weights (within 2^8 of the maximum), their sum
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    int bad = INT_MAX;   // the first prefix token whose scale of values is not finite
+    int bad = INT_MAX;   // the first prefix token with a large scale of values
 #pragma unroll
     for (int s = 0; s < S16; ++s)
 #pragma unroll
@@ -638,17 +648,18 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
       const uint32_t st = ws_a + uint32_t(c % NS) * L::kStage;
       const int tk = p.t0 + kTileChunk * (warp + NW * c);
 
-      // A row that ends before a token has weight 0 there, which a scale that is not
-      // finite would still make NaN: such scales enter as 0, and the rows that reach
-      // the first of them take NaN for their sum at the end. (A sequence's own tokens
-      // end for all rows together, behind them are zeros.)
+      // A row that ends before a token has weight 0 there, which a value past fp16
+      // would still make NaN: large scales enter as 0, and the rows that reach the
+      // first of them take NaN for their sum at the end. (A sequence's own tokens
+      // end for all rows together, behind them are zeros; a value past fp16 makes the
+      // sums infinite or NaN.)
       if (p.pre) {
         uint32_t any = 0;
 #pragma unroll
         for (int i = 0; i < (NG + 7) / 8; ++i) {
           const uint4 u = lds128(st + L::kVS + lane * L::SBS + 16 * i);
-          any |= nonfinite_halves(u.x) | nonfinite_halves(u.y) | nonfinite_halves(u.z) |
-                 nonfinite_halves(u.w);
+          any |= large_halves<BITS>(u.x) | large_halves<BITS>(u.y) | large_halves<BITS>(u.z) |
+                 large_halves<BITS>(u.w);
         }
         if (__any_sync(0xffffffffu, any != 0)) {
           if (any) {
@@ -805,9 +816,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
           mma_f16(O[s], a0, a1, a2, a3, ph[mt][0], ph[mt][1]);
           if constexpr (EXACT) mma_f16(O[s], a0, a1, a2, a3, pl[mt][0], pl[mt][1]);
         };
-        // fp16 1024 + u, or 1024 + 16 u, to c / 8 (int4) or c / 128 (exact)
-        constexpr uint32_t k8 = 0x30003000u, k128 = 0x20002000u;     // 2^-3, 2^-7
-        constexpr uint32_t o8 = 0xD808D808u, o128 = 0xC880C880u;     // -1032 / 8, -1152 / 128
+        // fp16 1024 + u, or 1024 + 16 u, to c (exact)
+        constexpr uint32_t k1 = 0x3C003C00u, k16 = 0x2C002C00u;                   // 1, 2^-4
+        constexpr uint32_t o8 = 0xE408E408u, o72 = 0xD480D480u, o128 = 0xE480E480u;   // -1032, -72, -1152
         if constexpr (BITS == 4) {
 #pragma unroll
           for (int s = 0; s < S16; s += 2) {
@@ -816,10 +827,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t y = r[i] >> 8;
-              weigh(s + i, hfma2((r[i] & 0x000F000Fu) ^ h_lo, k8, o8),
-                    hfma2((r[i] & 0x00F000F0u) ^ h_hi, k128, o128),
-                    hfma2((y & 0x000F000Fu) ^ h_lo, k8, o8),
-                    hfma2((y & 0x00F000F0u) ^ h_hi, k128, o128));
+              weigh(s + i, hfma2((r[i] & 0x000F000Fu) ^ h_lo, k1, o8),
+                    hfma2((r[i] & 0x00F000F0u) ^ h_hi, k16, o72),
+                    hfma2((y & 0x000F000Fu) ^ h_lo, k1, o8),
+                    hfma2((y & 0x00F000F0u) ^ h_hi, k16, o72));
             }
           }
         } else {
@@ -827,10 +838,10 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
           for (int s = 0; s < S16; ++s) {
             uint32_t r0, r1;
             ldmatrix_bytes_trans(r0, r1, vr + 16 * s);
-            weigh(s, hfma2((r0 & 0x00FF00FFu) ^ h_lo, k128, o128),
-                  hfma2((r1 & 0x00FF00FFu) ^ h_lo, k128, o128),
-                  hfma2(((r0 >> 8) & 0x00FF00FFu) ^ h_lo, k128, o128),
-                  hfma2(((r1 >> 8) & 0x00FF00FFu) ^ h_lo, k128, o128));
+            weigh(s, hfma2((r0 & 0x00FF00FFu) ^ h_lo, k1, o128),
+                  hfma2((r1 & 0x00FF00FFu) ^ h_lo, k1, o128),
+                  hfma2(((r0 >> 8) & 0x00FF00FFu) ^ h_lo, k1, o128),
+                  hfma2(((r1 >> 8) & 0x00FF00FFu) ^ h_lo, k1, o128));
           }
         }
       }
@@ -858,7 +869,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     }
 #pragma unroll
     for (int s = 0; s < S16; ++s) {
-      constexpr float f = BITS == 4 ? 0.0625f : 1.0f;   // C / 2^7
+      constexpr float f = 0x1p-7f;
       if constexpr (BITS == 4) {   // rows g, g + 8: coordinates 2g, 2g + 1
         float* o = wo + 2 * t * D + 16 * s + 2 * g;
         *reinterpret_cast<float2*>(o) = make_float2(O[s][0] * f, O[s][2] * f);
@@ -903,11 +914,86 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
   }
 }
 
+// Query head v of sequence b, KV head h, by a warp and in float32 throughout: the
+// form for scales that the parts' fp16 does not hold. The state is as the join has
+// it; its sum is NaN when the query or a token's scale is not finite. (Not inlined,
+// and the arguments stay in the constant bank, so that the join's own path keeps its
+// registers: with both in a stack frame a call took 5 us more.)
+template <int E>
+struct RowState {
+  float m, l;
+  float2 acc[E];
+};
+template <int ROT, int D>
+__device__ __noinline__ RowState<D / 64> attend_float32(const PrefixArgs& a, int64_t v, int b,
+                                                        int h) {
+  constexpr int E = D / 64;
+  RowState<E> r;
+  float m = -INFINITY, l = 0.0f;
+  float2 acc[E];
+  const int lane = threadIdx.x & 31, ng = D >> a.lg_group;
+  bool bad = false;   // a query or a scale that is not finite
+  float2 q[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    q[e] = reinterpret_cast<const float2*>(a.qrot + v * D)[warp_pair<ROT, D>(lane, e)];
+    acc[e] = make_float2(0.0f, 0.0f);
+    bad = bad || !(fabsf(q[e].x) < INFINITY && fabsf(q[e].y) < INFINITY);
+  }
+  const bool none = __any_sync(0xffffffffu, bad);   // nothing to be had
+  // coordinates 2k and 2k + 1 of a vector, times their scale
+  auto pair = [&](const uint8_t* codes, const uint16_t* scales, int64_t vec, int k, bool& bad) {
+    int c0, c1;
+    if (a.bits == 4) {
+      const int w = codes[vec * (D / 2) + k];
+      c0 = (w & 15) - ((w & 8) << 1);
+      c1 = (w >> 4) - ((w & 128) >> 3);
+    } else {
+      const int8_t* p = reinterpret_cast<const int8_t*>(codes) + vec * D + 2 * k;
+      c0 = p[0];
+      c1 = p[1];
+    }
+    const float s = __half2float(__ushort_as_half(scales[vec * ng + ((2 * k) >> a.lg_group)]));
+    bad = bad || !(fabsf(s) < INFINITY);
+    return make_float2(s * float(c0), s * float(c1));
+  };
+  const int32_t* own = a.block_table + int64_t(b) * a.max_pages;
+  const int len = none ? 0 : a.len(b);
+  for (int t = 0; t < len; ++t) {
+    const int64_t row = a.map.row(t < a.prefix_len ? a.prefix_table : own, uint32_t(t));
+    if (row < 0) continue;
+    const int64_t vec = row * a.heads + h;
+    float x = 0.0f;
+    float2 y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int k = warp_pair<ROT, D>(lane, e);
+      const float2 c = pair(a.k_codes, a.k_scales, vec, k, bad);
+      x = fmaf(q[e].x, c.x, fmaf(q[e].y, c.y, x));
+      y[e] = pair(a.v_codes, a.v_scales, vec, k, bad);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    const float top = fmaxf(m, x), ref = top == -INFINITY ? 0.0f : top;
+    const float f = exp2f(m - ref), p = exp2f(x - ref);
+    m = top;
+    l = fmaf(l, f, p);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      acc[e] = make_float2(fmaf(acc[e].x, f, p * y[e].x), fmaf(acc[e].y, f, p * y[e].y));
+  }
+  r.m = m;
+  r.l = __any_sync(0xffffffffu, bad) ? NAN : l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) r.acc[e] = acc[e];
+  return r;
+}
+
 // NW warps per query head, four heads to a block of the one-warp form. The parts'
 // (m, l) by all lanes, then their weighted sums, a warp a part in turn, added over
 // the warps in order; the rotation by the first warp.
 template <int ROT, int D, int NW>
-__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32) prefix_merge_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32) prefix_merge_kernel(const __grid_constant__ PrefixArgs a) {
   constexpr int E = D / 64;
   __shared__ float acc_sh[NW][D];
   __shared__ float2 ml_sh[NW];
@@ -983,15 +1069,31 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32) prefix_merge_kernel(c
       }
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : l;   // no token: 0 (a NaN stays)
-  const float2* lam = reinterpret_cast<const float2*>(a.v_lambda + int64_t(h) * D);
+  // on their way before the call below, which nothing is moved across
+  float2 lam[E];
+  int8_t sg[2 * E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const float2 f = lam[warp_pair<ROT, D>(lane, e)];
-    acc[e] = make_float2(acc[e].x * inv * f.x, acc[e].y * inv * f.y);
+    lam[e] = reinterpret_cast<const float2*>(a.v_lambda + int64_t(h) * D)[warp_pair<ROT, D>(lane, e)];
+    sg[2 * e] = a.v_signs[int64_t(h) * D + 2 * (E * lane + e)];
+    sg[2 * e + 1] = a.v_signs[int64_t(h) * D + 2 * (E * lane + e) + 1];
   }
+  bool finite = fabsf(l) < INFINITY;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    finite = finite && fabsf(acc[e].x) < INFINITY && fabsf(acc[e].y) < INFINITY;
+  if (!__all_sync(0xffffffffu, finite)) {
+    const RowState<E> r = attend_float32<ROT, D>(a, v, b, h);
+    m = r.m;
+    l = r.l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = r.acc[e];
+  }
+  const float inv = l > 0.0f ? 1.0f / l : l;   // no token: 0 (a NaN stays)
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    acc[e] = make_float2(acc[e].x * inv * lam[e].x, acc[e].y * inv * lam[e].y);
   warp_rotate_inverse<ROT, D>(acc, lane);
-  const int8_t* sg = a.v_signs + int64_t(h) * D + 2 * E * lane;
   uint32_t* o = reinterpret_cast<uint32_t*>(a.out) + v * (D / 2) + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) {

@@ -3,14 +3,11 @@
 //
 // A block takes 128 query rows (of all sequences) of one head and a range of
 // the prefix's tokens, TN at a time:
-//   S[row][token]  = Q (sigma c / C)^T        both operands in shared memory,
-//                    C = 8 (int4) or 128 (int8);
+//   S[row][token]  = Q (sigma c)^T            both operands in shared memory;
 //   P[row][token]  = 2^7 e^{x - ref}, fp16, written over S in tensor memory;
-//   O[row][coord] += P (sigma c / C)          P from tensor memory.
-// Warps 4-7 turn packed codes into swizzled fp16 tiles (sigma c / C, rounded
-// once: at most |sigma|, so it cannot overflow, and no smaller than that
-// allows), warp 8 issues the products,
-// warps 0-3 hold a query row per thread: its maximum and sum need no exchange.
+//   O[row][coord] += P (sigma c)              P from tensor memory.
+// Warps 4-7 turn packed codes into swizzled fp16 tiles (sigma c, rounded once:
+// kLargeScale), warp 8 issues the products, warps 0-3 hold a query row per thread: its maximum and sum need no exchange.
 // Two score buffers let the tensor cores form the next scores while the
 // exponentials of these are taken. O is rescaled only when a row's maximum
 // grows by more than 2^8 over the reference its weights use (the weights then
@@ -73,10 +70,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// What decoded codes are divided by, a power of two >= |c|.
-template <int BITS>
-constexpr float kCodeUnit = BITS == 4 ? 8.0f : 128.0f;
-
 // Position p of 8 consecutive coordinates in the decoded order: the code pairs
 // that one AND isolates. int4: (0, 4), (1, 5), (2, 6), (3, 7); int8, two words of
 // 4: (0, 2), (1, 3) each.
@@ -85,26 +78,26 @@ __host__ __device__ constexpr int decoded_coord(int p) {
   return BITS == 4 ? (p & 1) * 4 + (p >> 1) : (p & 4) + 2 * (p & 1) + ((p >> 1) & 1);
 }
 
-// 8 codes (1 or 2 words) to sigma c / kCodeUnit in decoded order: v rounded to fp16,
-// rest what that left (exact, but for subnormals). h_lo, h_hi: the magic numbers
-// 1024 + u and 1024 + 16 u in registers.
+// 8 codes (1 or 2 words) to sigma c in decoded order: v rounded to fp16, rest what
+// that left (exact: a product has 18 bits at most). h_lo, h_hi: the magic numbers
+// 1024 + u and 1024 + 16 u (int8: 1024 + u) in registers.
 template <int BITS, bool REST>
 __device__ __forceinline__ void decode_chunk(const uint32_t* w, uint32_t sg2, uint32_t h_lo,
                                              uint32_t h_hi, uint4& v, uint4& rest) {
-  constexpr uint32_t k8 = 0x30003000u, k128 = 0x20002000u;   // 2^-3, 2^-7
-  constexpr uint32_t o8 = 0xD808D808u, o128 = 0xC880C880u;   // -1032 / 8, -1152 / 128
+  constexpr uint32_t k1 = 0x3C003C00u, k16 = 0x2C002C00u;                       // 1, 2^-4
+  constexpr uint32_t o8 = 0xE408E408u, o72 = 0xD480D480u, o128 = 0xE480E480u;   // -1032, -72, -1152
   uint32_t c[4];
   if constexpr (BITS == 4) {
     const uint32_t y = w[0] >> 8;
-    c[0] = hfma2((w[0] & 0x000F000Fu) ^ h_lo, k8, o8);
-    c[1] = hfma2((w[0] & 0x00F000F0u) ^ h_hi, k128, o128);   // 16 c / 128
-    c[2] = hfma2((y & 0x000F000Fu) ^ h_lo, k8, o8);
-    c[3] = hfma2((y & 0x00F000F0u) ^ h_hi, k128, o128);
+    c[0] = hfma2((w[0] & 0x000F000Fu) ^ h_lo, k1, o8);
+    c[1] = hfma2((w[0] & 0x00F000F0u) ^ h_hi, k16, o72);
+    c[2] = hfma2((y & 0x000F000Fu) ^ h_lo, k1, o8);
+    c[3] = hfma2((y & 0x00F000F0u) ^ h_hi, k16, o72);
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      c[2 * i] = hfma2((w[i] & 0x00FF00FFu) ^ h_hi, k128, o128);
-      c[2 * i + 1] = hfma2(((w[i] >> 8) & 0x00FF00FFu) ^ h_hi, k128, o128);
+      c[2 * i] = hfma2((w[i] & 0x00FF00FFu) ^ h_hi, k1, o128);
+      c[2 * i + 1] = hfma2(((w[i] >> 8) & 0x00FF00FFu) ^ h_hi, k1, o128);
     }
   }
   v = make_uint4(hmul2(c[0], sg2), hmul2(c[1], sg2), hmul2(c[2], sg2), hmul2(c[3], sg2));
@@ -160,20 +153,20 @@ __device__ __forceinline__ void decode_pieces(uint32_t base, uint32_t rest_at, i
   }
 }
 
-// Scales that are not finite may belong to tokens behind the end of some rows,
-// whose weights there are 0 and would still make NaN of them. So they enter the
-// products as 0, and the first token that has one goes to shared memory; the rows
-// that reach it take NaN for their sum at the end (each attends to all tokens
-// below its length, so the first is enough).
-template <int NK, class Tok>
-__device__ __forceinline__ void drop_nonfinite(uint32_t (&s)[NK], int* first_bad, Tok token) {
+// Large scales (kLargeScale) may belong to tokens behind the end of some rows, whose
+// weights there are 0 and would still make NaN of them. So they enter the products as
+// 0, and the first token that has one goes to shared memory; the rows that reach it
+// take NaN for their sum at the end (each attends to all tokens below its length, so
+// the first is enough), and the join does them anew.
+template <int BITS, int NK, class Tok>
+__device__ __forceinline__ void drop_large(uint32_t (&s)[NK], int* first_bad, Tok token) {
   uint32_t any = 0;
 #pragma unroll
-  for (int k = 0; k < NK; ++k) any |= nonfinite_halves(s[k]);
+  for (int k = 0; k < NK; ++k) any |= large_halves<BITS>(s[k]);
   if (any) {
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const uint32_t bad = nonfinite_halves(s[k]);
+      const uint32_t bad = large_halves<BITS>(s[k]);
       if (bad) {
         s[k] &= ~((bad >> 15) * 0xFFFFu);
         atomicMin(first_bad, token(k));
@@ -353,7 +346,7 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < NK; ++k) on_sh[(i & 3) * TN + tr + k * RPP] = row[k] >= 0 ? 1 : 0;
       }
-      drop_nonfinite(ks, first_bad, [&](int k) { return token(i, k); });
+      drop_large<BITS>(ks, first_bad, [&](int k) { return token(i, k); });
       decode_pieces<D, BITS, G, TN, EXACT, NK>(sm + L::kKOff + st * L::kKT, L::kT, pc, tr, kw, ks, h_lo,
                                            h_hi);
       __threadfence_block();
@@ -364,7 +357,7 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
       if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&vempty[st], ((i >> 1) & 1) ^ 1,
                                                            abort_flag, a.guard)))
         break;
-      drop_nonfinite(vs, first_bad, [&](int k) { return token(i, k); });
+      drop_large<BITS>(vs, first_bad, [&](int k) { return token(i, k); });
       decode_pieces<D, BITS, G, TN, false, NK>(sm + L::kVOff + st * L::kT, 0, pc, tr, vw, vs, h_lo,
                                            h_hi);
       fence_proxy_async_smem();
@@ -500,8 +493,7 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
           float y[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            y[(j & ~7) + decoded_coord<BITS>(j & 7)] =
-                __uint_as_float(o[j]) * (kCodeUnit<BITS> * 0x1p-7f);
+            y[(j & ~7) + decoded_coord<BITS>(j & 7)] = __uint_as_float(o[j]) * 0x1p-7f;
           float4* dst = reinterpret_cast<float4*>(a.pre_acc + part * D + k);
 #pragma unroll
           for (int j = 0; j < 8; ++j)

@@ -3,10 +3,9 @@
 //
 // A unit is 128 query rows with two score tiles S, the weights P written over
 // them, and an accumulator O, all in tensor memory:
-//   S[row][token]  = Q (sigma c / C)^T        TN = 64 tokens at a time, C = 8
-//                    (int4) or 128 (int8);
+//   S[row][token]  = Q (sigma c)^T            TN = 64 tokens at a time;
 //   P[row][token]  = 2^7 e^{x - ref}, fp16, written over S;
-//   O[row][coord] += P (sigma c / C).
+//   O[row][coord] += P (sigma c).
 // The scores of a unit's next tile are formed while its four warps take the
 // exponentials of this one. Two forms:
 //   shared   the units are 256 different rows over the same tokens: a token's
@@ -15,8 +14,8 @@
 //            softmax (up to 128 rows, and fp16 outputs).
 //
 // Warps 0-3 and 4-7: softmax of unit 0 and 1, a query row per thread. Warps
-// 8-11 and 12-15: codes of keys and of values to fp16 tiles (swizzled, sigma c /
-// C rounded once: at most |sigma|, so it cannot overflow). Warps 16 and 17:
+// 8-11 and 12-15: codes of keys and of values to fp16 tiles (swizzled, sigma c
+// rounded once: kLargeScale). Warps 16 and 17:
 // issue the units' products. Warps 18 and 19: copy codes and scales of a tile
 // each in turn into a ring of raw stages, so that memory latency is hidden by
 // depth, not by registers. O is rescaled only when a row's maximum grows by more
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
           s[k] = x;
         }
       }
-      drop_nonfinite(s, first_bad, [&](int k) { return t0 + j * TN + tr + k * RPP; });
+      drop_large<BITS>(s, first_bad, [&](int k) { return t0 + j * TN + tr + k * RPP; });
       // an entry of the ring is written again 16 tiles on, long after the
       // softmax of this tile: at most the slots' tiles lie between
       if (tid == 256) {
@@ -477,8 +476,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
             float y[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              y[(i & ~7) + decoded_coord<BITS>(i & 7)] =
-                  __uint_as_float(o[i]) * (kCodeUnit<BITS> * 0x1p-7f);
+              y[(i & ~7) + decoded_coord<BITS>(i & 7)] = __uint_as_float(o[i]) * 0x1p-7f;
             float4* dst = reinterpret_cast<float4*>(a.pre_acc + part * D + k);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
