@@ -334,6 +334,10 @@ __device__ __forceinline__ void ldmatrix_bytes_trans(uint32_t& r0, uint32_t& r1,
 // Calibrated scales are of order one; only vectors next to fp16's own end reach it.
 template <int BITS>
 constexpr uint32_t kLargeScale = BITS == 4 ? 0x7000u : 0x6000u;
+// 0x8000 in each half that is an infinite or NaN fp16.
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t s) {
+  return ((s & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
 // 0x8000 in each half whose magnitude is at least that, infinite or NaN.
 template <int BITS>
 __device__ __forceinline__ uint32_t large_halves(uint32_t s) {
@@ -914,53 +918,84 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
   }
 }
 
-// Query head v of sequence b, KV head h, by a warp and in float32 throughout: the
-// form for scales that the parts' fp16 does not hold. The state is as the join has
-// it; its sum is NaN when the query or a token's scale is not finite. (Not inlined,
-// and the arguments stay in the constant bank, so that the join's own path keeps its
-// registers: with both in a stack frame a call took 5 us more.)
+// A query head whose sums are not finite, by a warp: either its query or a scale is
+// not, and NaN is the answer; or a scale is larger than the parts' fp16 holds
+// (kLargeScale), and the head is done anew, in float32. (Neither function is inlined,
+// the arguments stay in the constant bank and the join's blocks per SM are stated, so
+// that its own path keeps its registers: with a stack frame, or with all warps of the
+// join in here, a call of the attention took 1 to 5 us more.)
+template <int NW>
+__device__ __forceinline__ int64_t merged_row() {
+  return NW == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+}
+template <int D, int NW>
+__device__ __noinline__ bool row_is_finite(const PrefixArgs& a) {
+  const int64_t v = merged_row<NW>();
+  const int hq = a.heads * a.q_per_kv, b = int(v / hq), h = int(v % hq) / a.q_per_kv;
+  const int lane = threadIdx.x & 31, ng = D >> a.lg_group, len = a.len(b);
+  bool ok = true;
+  for (int k = lane; k < D; k += 32) ok = ok && fabsf(a.qrot[v * D + k]) < INFINITY;
+  // the scales, a token to a lane (positions below 2^31 - 65536)
+  for (int t = lane; __all_sync(0xffffffffu, ok) && t - lane < len; t += 32) {
+    const int32_t* table = t < a.prefix_len ? a.prefix_table : a.block_table + int64_t(b) * a.max_pages;
+    const int64_t row = t < len ? a.map.row(table, uint32_t(t)) : -1;
+    if (row < 0) continue;
+    const int64_t at = (row * a.heads + h) * ng;
+    if (ng >= 8) {
+      for (int i = 0; i < ng; i += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(a.k_scales + at + i);
+        const uint4 y = *reinterpret_cast<const uint4*>(a.v_scales + at + i);
+        ok = ok && !(nonfinite_halves(x.x) | nonfinite_halves(x.y) | nonfinite_halves(x.z) |
+                     nonfinite_halves(x.w) | nonfinite_halves(y.x) | nonfinite_halves(y.y) |
+                     nonfinite_halves(y.z) | nonfinite_halves(y.w));
+      }
+    } else {
+      for (int i = 0; i < ng; ++i)
+        ok = ok && !nonfinite_halves(a.k_scales[at + i] | uint32_t(a.v_scales[at + i]) << 16);
+    }
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// Codes of coordinates 2k and 2k + 1 of vector vec, times their scale.
+template <int D>
+__device__ __forceinline__ float2 decoded_pair(const PrefixArgs& a, const uint8_t* codes,
+                                               const uint16_t* scales, int64_t vec, int k) {
+  const float f = __half2float(
+      __ushort_as_half(scales[vec * (D >> a.lg_group) + ((2 * k) >> a.lg_group)]));
+  int c0, c1;
+  if (a.bits == 4) {
+    const int w = codes[vec * (D / 2) + k];
+    c0 = (w & 15) - ((w & 8) << 1);
+    c1 = (w >> 4) - ((w & 128) >> 3);
+  } else {
+    const int8_t* p = reinterpret_cast<const int8_t*>(codes) + vec * D + 2 * k;
+    c0 = p[0];
+    c1 = p[1];
+  }
+  return make_float2(f * float(c0), f * float(c1));
+}
+
 template <int E>
 struct RowState {
   float m, l;
-  float2 acc[E];
+  float2 acc[E];   // the pairs warp_pair(lane, e)
 };
-template <int ROT, int D>
-__device__ __noinline__ RowState<D / 64> attend_float32(const PrefixArgs& a, int64_t v, int b,
-                                                        int h) {
+template <int ROT, int D, int NW>
+__device__ __noinline__ RowState<D / 64> attend_float32(const PrefixArgs& a) {
   constexpr int E = D / 64;
-  RowState<E> r;
-  float m = -INFINITY, l = 0.0f;
-  float2 acc[E];
-  const int lane = threadIdx.x & 31, ng = D >> a.lg_group;
-  bool bad = false;   // a query or a scale that is not finite
-  float2 q[E];
+  const int64_t v = merged_row<NW>();
+  const int hq = a.heads * a.q_per_kv, b = int(v / hq), h = int(v % hq) / a.q_per_kv;
+  const int lane = threadIdx.x & 31, len = a.len(b);
+  RowState<E> s;
+  s.m = -INFINITY;
+  s.l = 0.0f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = reinterpret_cast<const float2*>(a.qrot + v * D)[warp_pair<ROT, D>(lane, e)];
-    acc[e] = make_float2(0.0f, 0.0f);
-    bad = bad || !(fabsf(q[e].x) < INFINITY && fabsf(q[e].y) < INFINITY);
-  }
-  const bool none = __any_sync(0xffffffffu, bad);   // nothing to be had
-  // coordinates 2k and 2k + 1 of a vector, times their scale
-  auto pair = [&](const uint8_t* codes, const uint16_t* scales, int64_t vec, int k, bool& bad) {
-    int c0, c1;
-    if (a.bits == 4) {
-      const int w = codes[vec * (D / 2) + k];
-      c0 = (w & 15) - ((w & 8) << 1);
-      c1 = (w >> 4) - ((w & 128) >> 3);
-    } else {
-      const int8_t* p = reinterpret_cast<const int8_t*>(codes) + vec * D + 2 * k;
-      c0 = p[0];
-      c1 = p[1];
-    }
-    const float s = __half2float(__ushort_as_half(scales[vec * ng + ((2 * k) >> a.lg_group)]));
-    bad = bad || !(fabsf(s) < INFINITY);
-    return make_float2(s * float(c0), s * float(c1));
-  };
-  const int32_t* own = a.block_table + int64_t(b) * a.max_pages;
-  const int len = none ? 0 : a.len(b);
+  for (int e = 0; e < E; ++e) s.acc[e] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
   for (int t = 0; t < len; ++t) {
-    const int64_t row = a.map.row(t < a.prefix_len ? a.prefix_table : own, uint32_t(t));
+    const int32_t* table = t < a.prefix_len ? a.prefix_table : a.block_table + int64_t(b) * a.max_pages;
+    const int64_t row = a.map.row(table, uint32_t(t));
     if (row < 0) continue;
     const int64_t vec = row * a.heads + h;
     float x = 0.0f;
@@ -968,39 +1003,37 @@ __device__ __noinline__ RowState<D / 64> attend_float32(const PrefixArgs& a, int
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int k = warp_pair<ROT, D>(lane, e);
-      const float2 c = pair(a.k_codes, a.k_scales, vec, k, bad);
-      x = fmaf(q[e].x, c.x, fmaf(q[e].y, c.y, x));
-      y[e] = pair(a.v_codes, a.v_scales, vec, k, bad);
+      const float2 z = reinterpret_cast<const float2*>(a.qrot + v * D)[k];
+      const float2 c = decoded_pair<D>(a, a.k_codes, a.k_scales, vec, k);
+      x = fmaf(z.x, c.x, fmaf(z.y, c.y, x));
+      y[e] = decoded_pair<D>(a, a.v_codes, a.v_scales, vec, k);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    const float top = fmaxf(m, x), ref = top == -INFINITY ? 0.0f : top;
-    const float f = exp2f(m - ref), p = exp2f(x - ref);
-    m = top;
-    l = fmaf(l, f, p);
+    const float top = fmaxf(s.m, x), f = exp2f(s.m - top), p = exp2f(x - top);
+    s.m = top;
+    s.l = fmaf(s.l, f, p);
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      acc[e] = make_float2(fmaf(acc[e].x, f, p * y[e].x), fmaf(acc[e].y, f, p * y[e].y));
+      s.acc[e] = make_float2(fmaf(s.acc[e].x, f, p * y[e].x), fmaf(s.acc[e].y, f, p * y[e].y));
   }
-  r.m = m;
-  r.l = __any_sync(0xffffffffu, bad) ? NAN : l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) r.acc[e] = acc[e];
-  return r;
+  return s;
 }
 
 // NW warps per query head, four heads to a block of the one-warp form. The parts'
 // (m, l) by all lanes, then their weighted sums, a warp a part in turn, added over
 // the warps in order; the rotation by the first warp.
 template <int ROT, int D, int NW>
-__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32) prefix_merge_kernel(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
+                                  NW == 16 ? (D == 256 ? 1 : 2) : (D == 256 ? 5 : 8))
+    prefix_merge_kernel(const __grid_constant__ PrefixArgs a) {
   constexpr int E = D / 64;
   __shared__ float acc_sh[NW][D];
   __shared__ float2 ml_sh[NW];
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : int(threadIdx.x >> 5);
   const int g = a.q_per_kv, hq = a.heads * g;
-  const int64_t v = NW == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+  const int64_t v = merged_row<NW>();
   if (NW == 1 && v >= int64_t(a.n_seq) * hq) return;
   const int b = int(v / hq), h = int(v % hq) / g, j = int(v % hq) % g;
   const int64_t M = int64_t(a.n_seq) * g;
@@ -1083,11 +1116,14 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32) prefix_merge_kernel(c
   for (int e = 0; e < E; ++e)
     finite = finite && fabsf(acc[e].x) < INFINITY && fabsf(acc[e].y) < INFINITY;
   if (!__all_sync(0xffffffffu, finite)) {
-    const RowState<E> r = attend_float32<ROT, D>(a, v, b, h);
-    m = r.m;
-    l = r.l;
+    l = NAN;
+    if (row_is_finite<D, NW>(a)) {
+      const RowState<E> s = attend_float32<ROT, D, NW>(a);
+      m = s.m;
+      l = s.l;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = r.acc[e];
+      for (int e = 0; e < E; ++e) acc[e] = s.acc[e];
+    }
   }
   const float inv = l > 0.0f ? 1.0f / l : l;   // no token: 0 (a NaN stays)
 #pragma unroll
