@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cstdint>
 #include <mutex>
 
@@ -117,7 +118,7 @@ int check_prefix_sizes(const srftq_desc* desc, int64_t n_seq, int32_t q_per_kv,
   if (rc != SRFTQ_OK) return rc;
   if (n_seq < 0 || prefix_len < 0 || q_per_kv < 1) return SRFTQ_ERR_INVALID_ARG;
   if (q_per_kv > 16 || prefix_len >= kMaxPosition || n_seq >= kMaxPosition / 16 ||
-      desc->heads >= (1 << 20))
+      desc->heads >= (1 << 20) || n_seq * desc->heads * q_per_kv > INT_MAX)
     return SRFTQ_ERR_UNSUPPORTED;
   return SRFTQ_OK;
 }

@@ -149,9 +149,8 @@ int launch_prefix_attention(const PrefixAttnCall& c) {
   a.own_acc = reinterpret_cast<float*>(ws + s.own_acc_off);
   a.guard = Runtime::guard_word();
   if (!a.guard) return SRFTQ_ERR_CUDA;
-  const int64_t queries = c.n_seq * c.heads * c.q_per_kv;
-  const int64_t blocks = (queries + 7) / 8;   // a warp per query
-  if (queries > INT_MAX) return SRFTQ_ERR_UNSUPPORTED;
+  const int64_t queries = c.n_seq * c.heads * c.q_per_kv;   // below 2^31 (check_prefix_sizes)
+  const int64_t blocks = (queries + 7) / 8;                 // a warp per query
   int rc = SRFTQ_ERR_UNSUPPORTED;
   static_for<6, 9>([&](auto lg_) {
     constexpr int D = 1 << decltype(lg_)::value;
