@@ -115,6 +115,12 @@ __device__ __forceinline__ int64_t vec_limit(int64_t S, int64_t stride, int64_t 
   return ((S - 1) * stride + N) * H;
 }
 
+// Paged calls: vector v of pools of `rows` rows a slice (debug checks).
+__device__ __forceinline__ bool dbg_slot(size_t v, const TileGeom& g, int64_t rows,
+                                         unsigned* guard) {
+  return dbg_ok(int64_t(v) < vec_limit(g.n_slices, rows, rows, g.heads), guard);
+}
+
 // The tile a TMA copy addresses lies inside the call's extents (debug checks).
 __device__ __forceinline__ bool tile_in_range(const TileWalk& c, const TileGeom& g) {
   return c.s >= 0 && c.s < g.n_slices && c.hb >= 0 && c.hb < g.head_blocks && c.rb >= 0 &&
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     const size_t vec = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
                         (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) * a.g.heads +
                        cur.hb * hpt + hl;
-    const bool valid = PAGED ? slot >= 0 :
+    const bool valid = PAGED ? slot >= 0 && dbg_slot(vec, a.g, a.out_slice_stride_rows, a.guard) :
         row < a.g.n_rows &&
         dbg_ok(int64_t(vec) < vec_limit(a.g.n_slices, a.out_slice_stride_rows, a.g.n_rows,
                                         a.g.heads),
@@ -686,7 +692,8 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
                                  piece * (S::TR * S::C_SPAN));
           const size_t v_to = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
                                (to < 0 ? 0 : to)) * a.g.heads + cur.hb * hpt + (src & (hpt - 1));
-          if (to >= 0) reinterpret_cast<uint4*>(a.codes + v_to * S::CB)[ci] = w;
+          if (to >= 0 && dbg_slot(v_to, a.g, a.out_slice_stride_rows, a.guard))
+            reinterpret_cast<uint4*>(a.codes + v_to * S::CB)[ci] = w;
         }
       } else {
         fence_proxy_async_smem();
@@ -803,9 +810,9 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
       const int i = lane + 32 * k, src = i / CPV, ci = i % CPV;
       const int64_t from = __shfl_sync(0xffffffffu, slot, src);
       const int piece = (ci * 16) / S::C_SPAN, cc = ((ci * 16) % S::C_SPAN) / 16;
-      if (from >= 0) {
-        const size_t v = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + from) * a.g.heads +
-                         c.hb * hpt + (src & (hpt - 1));
+      const size_t v = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + (from < 0 ? 0 : from)) *
+                           a.g.heads + c.hb * hpt + (src & (hpt - 1));
+      if (from >= 0 && dbg_slot(v, a.g, a.in_slice_stride_rows, a.guard)) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                          swz_chunk<S::C_SPAN>(swz_row<S::C_SPAN>(smem_addr(ws), src), cc) +
                          piece * (S::TR * S::C_SPAN)),
@@ -864,7 +871,7 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     const size_t vec = (static_cast<size_t>(c.s) * a.in_slice_stride_rows +
                         (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) * a.g.heads +
                        c.hb * hpt + hl;
-    if (PAGED ? slot >= 0 : row < a.g.n_rows &&
+    if (PAGED ? slot >= 0 && dbg_slot(vec, a.g, a.in_slice_stride_rows, a.guard) : row < a.g.n_rows &&
         dbg_ok(int64_t(vec) < vec_limit(a.g.n_slices, a.in_slice_stride_rows, a.g.n_rows,
                                         a.g.heads),
                a.guard)) {
@@ -1034,7 +1041,7 @@ __global__ void __launch_bounds__(WPC * 32, MINB)
     if constexpr (PAGED) {
       if (!__all_sync(0xffffffffu, valid || row >= a.g.n_rows)) {
         pending = false;   // rows to leave alone: each lane stores its own vector
-        if (valid) {
+        if (valid && dbg_ok(row < a.g.n_rows, a.guard)) {
           uint16_t* dst = a.xhat + ((static_cast<size_t>(cur.s) * a.out_slice_stride_rows + row) *
                                         a.g.heads + cur.hb * hpt + hl) * D;
           static_for<0, D / 8>([&](auto c_) {

@@ -648,7 +648,8 @@ __global__ void __launch_bounds__(64, MINB)
         const uint4 w = lds128(code_chunk_addr<S>(swz_row<S::C_SPAN>(smem_addr(ob), src), ci));
         const size_t v_to = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
                              (to < 0 ? 0 : to)) * a.g.heads + cur.hb * hpt + (src & (hpt - 1));
-        if (to >= 0) reinterpret_cast<uint4*>(a.codes + v_to * S::CB)[ci] = w;
+        if (to >= 0 && dbg_slot(v_to, a.g, a.out_slice_stride_rows, a.guard))
+          reinterpret_cast<uint4*>(a.codes + v_to * S::CB)[ci] = w;
       }
     } else {
       fence_proxy_async_smem();
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(64, MINB)
     const size_t svec = (static_cast<size_t>(cur.s) * a.out_slice_stride_rows +
                          (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) *
                             a.g.heads + cur.hb * hpt + hl;
-    if (PAGED ? slot >= 0 : row < a.g.n_rows &&
+    if (PAGED ? slot >= 0 && dbg_slot(svec, a.g, a.out_slice_stride_rows, a.guard) : row < a.g.n_rows &&
         dbg_ok(int64_t(svec) < vec_limit(a.g.n_slices, a.out_slice_stride_rows, a.g.n_rows,
                                          a.g.heads),
                a.guard)) {
@@ -804,9 +805,9 @@ __global__ void __launch_bounds__(64, MINB)
     for (int k = 0; k < CPV / 2; ++k) {
       const int i = tid + 64 * k, src = i / CPV, ci = i % CPV;
       const int64_t from = __shfl_sync(0xffffffffu, slot, src);
-      if (from >= 0) {
-        const size_t v = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + from) * a.g.heads +
-                         c.hb * hpt + (src & (hpt - 1));
+      const size_t v = (static_cast<size_t>(c.s) * a.in_slice_stride_rows + (from < 0 ? 0 : from)) *
+                           a.g.heads + c.hb * hpt + (src & (hpt - 1));
+      if (from >= 0 && dbg_slot(v, a.g, a.in_slice_stride_rows, a.guard)) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                          code_chunk_addr<S>(swz_row<S::C_SPAN>(smem_addr(sb), src), ci)),
                      "l"(a.codes + v * S::CB + 16 * ci)
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(64, MINB)
     const size_t svec = (static_cast<size_t>(c.s) * a.in_slice_stride_rows +
                          (PAGED ? (slot < 0 ? 0 : slot) : int64_t(row))) * a.g.heads +
                         c.hb * hpt + hl;
-    if (PAGED ? slot >= 0 : row < a.g.n_rows &&
+    if (PAGED ? slot >= 0 && dbg_slot(svec, a.g, a.in_slice_stride_rows, a.guard) : row < a.g.n_rows &&
         dbg_ok(int64_t(svec) < vec_limit(a.g.n_slices, a.in_slice_stride_rows, a.g.n_rows,
                                          a.g.heads),
                a.guard)) {
@@ -1117,7 +1118,7 @@ __global__ void __launch_bounds__(64, MINB)
       if (!__all_sync(0xffffffffu, slot_cur >= 0 || row >= a.g.n_rows)) {
         pending = false;   // rows to leave alone: each warp stores half of its lanes' vectors
         bar_pair();
-        if (slot_cur >= 0) {
+        if (slot_cur >= 0 && dbg_ok(row < a.g.n_rows, a.guard)) {
           uint16_t* dst = a.xhat + ((static_cast<size_t>(cur.s) * a.out_slice_stride_rows + row) *
                                         a.g.heads + cur.hb * hpt + hl) * D;
 #pragma unroll 4

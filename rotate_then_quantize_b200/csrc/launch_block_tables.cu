@@ -42,6 +42,11 @@ struct TableArgs {
   int32_t* seq_lens;
   int32_t* row_start;
   int32_t* counts;
+  unsigned* guard;
+  // Index check of the debug build: the entry of page pg of sequence b.
+  __device__ __forceinline__ bool dbg_entry(int64_t b, int64_t pg) const {
+    return dbg_ok(b >= 0 && b < n_seq && pg >= 0 && pg < max_pages, guard);
+  }
 };
 
 __device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane) {
@@ -124,12 +129,13 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TableAr
       int32_t id = -1;
       if (pg < a.max_pages) {
         if (pg < at) {
-          id = a.table[(int64_t(b0) + i) * a.max_pages + pg];
+          if (a.dbg_entry(int64_t(b0) + i, pg)) id = a.table[(int64_t(b0) + i) * a.max_pages + pg];
         } else {
           const int64_t k = pages[i] + (pg - at);
           id = k < a.n_free ? a.free_pages[k] : -1;
         }
       }
+      if (!dbg_ok(r >= 0 && r < a.n_slots, a.guard)) continue;
       a.slots[r] = id >= 0 ? int64_t(id) * a.page.d + (pos - int64_t(pg) * a.page.d) : -1;
     }
     // this block's pages of [page0, page1)
@@ -139,6 +145,7 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TableAr
       if (k < page0 || k >= page1) continue;
       const int i = last_at_most(pages, n, k);
       const int32_t at = held[i] ? int32_t(a.page.div(uint32_t(held[i] - 1))) + 1 : 0;
+      if (!a.dbg_entry(int64_t(b0) + i, at + (k - pages[i]))) continue;
       a.table[(int64_t(b0) + i) * a.max_pages + at + (k - pages[i])] =
           k < a.n_free ? a.free_pages[k] : -1;
     }
@@ -161,7 +168,8 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TableAr
 int launch_block_tables(const BlockTablesCall& c) {
   TableArgs a{int32_t(c.n_seq), c.cached_lens, c.new_lens, FastDiv::make(uint32_t(c.page_size)),
               c.free_pages,     c.n_free,      c.block_table, int32_t(c.max_pages), c.slots,
-              c.n_slots,        c.seq_lens,    c.row_start,   c.counts};
+              c.n_slots,        c.seq_lens,    c.row_start,   c.counts, Runtime::guard_word()};
+  if (!a.guard) return SRFTQ_ERR_CUDA;
   // a block for each 1024 slots, up to two per SM (each scans all lengths)
   const int64_t want = (c.n_slots + kTabThreads - 1) / kTabThreads;
   const int64_t cap = 2 * int64_t(Runtime::num_sms());

@@ -98,6 +98,31 @@ struct PrefixArgs {
     return n < 0 ? 0 : n > most ? int32_t(most) : n;
   }
   __device__ __forceinline__ int32_t own(int b) const { return max(len(b) - prefix_len, 0); }
+
+  // Index checks of the debug build: a token's table entry (the prefix's table or a
+  // sequence's), a row of the pool, a query head, a chunk record, a row of the parts.
+  __device__ __forceinline__ bool dbg_token(bool pre, int64_t t) const {
+    return dbg_ok(t >= 0 && t < (pre ? int64_t(prefix_len) : int64_t(max_pages) * map.page.d), guard);
+  }
+  __device__ __forceinline__ bool dbg_row(int64_t row) const {
+    return dbg_ok(row >= 0 && row < int64_t(map.n_pages) * map.page.d, guard);
+  }
+  __device__ __forceinline__ bool dbg_query(int64_t v) const {
+    return dbg_ok(v >= 0 && v < int64_t(n_seq) * heads * q_per_kv, guard);
+  }
+  __device__ __forceinline__ bool dbg_chunk(int64_t c) const {
+    return dbg_ok(c >= 0 && c < int64_t(chunk_goal) + n_seq, guard);
+  }
+  __device__ __forceinline__ bool dbg_part(bool pre, int64_t part) const {
+    const int64_t chunks = int64_t(chunk_goal) + n_seq, rows = int64_t(n_seq) * q_per_kv;
+    return dbg_ok(part >= 0 && part < heads * (pre ? prefix_splits * rows : chunks * q_per_kv), guard);
+  }
+  // Pool row of token t, -1 when it has none.
+  __device__ __forceinline__ int64_t pool_row(bool pre, const int32_t* table, uint32_t t) const {
+    if (!dbg_token(pre, t)) return -1;
+    const int64_t row = map.row(table, t);
+    return row < 0 || dbg_row(row) ? row : -1;
+  }
 };
 
 __device__ __forceinline__ float lo_f32(uint32_t w, bool bf16) {
@@ -163,7 +188,7 @@ __device__ inline void plan_own_tokens(const PrefixArgs& a) {
     int4* o = a.chunk_of + a.chunk_start[b];   // this thread wrote it
     for (int32_t c = 0; c < n; ++c) {
       const int32_t t0 = a.prefix_len + c * chunk;
-      o[c] = make_int4(b, t0, range_end(t0, chunk, end), 0);
+      if (a.dbg_chunk(o + c - a.chunk_of)) o[c] = make_int4(b, t0, range_end(t0, chunk, end), 0);
     }
   }
   if (tid == 0) {
@@ -220,6 +245,7 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
   const float f = a.scale * kLog2e;
   for (int64_t v = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; v < total;
        v += (int64_t(gridDim.x) * blockDim.x) >> 5) {
+    if (!a.dbg_query(v)) continue;
     const int h = int(v % hq) / a.q_per_kv;
     const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + v * (D / 2) + lane * E;
     const int8_t* sg = a.k_signs + int64_t(h) * D + 2 * E * lane;
@@ -488,8 +514,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
   __shared__ int32_t next_sh;
   __shared__ int4 rec_sh;
   auto record = [&](int64_t i) {
-    return i >= n_pre && i < n_items ? a.chunk_of[own_chunk(a, i - n_pre, own_tiles)]
-                                     : make_int4(0, 0, 0, 0);
+    if (i < n_pre || i >= n_items) return make_int4(0, 0, 0, 0);
+    const int64_t c = own_chunk(a, i - n_pre, own_tiles);
+    return a.dbg_chunk(c) ? a.chunk_of[c] : make_int4(0, 0, 0, 0);
   };
   int4 rec = record(blockIdx.x);
   for (int64_t it = blockIdx.x; it < n_items;) {
@@ -516,7 +543,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
     // pool row of this lane's token of chunk c, -1 for none
     auto row_of = [&](int c) {
       const int tok = p.t0 + kTileChunk * (warp + NW * c) + lane;
-      return c < n_chunks && tok < p.t1 ? int32_t(a.map.row(p.table, uint32_t(tok))) : -1;
+      return c < n_chunks && tok < p.t1 ? int32_t(a.pool_row(p.pre, p.table, uint32_t(tok))) : -1;
     };
     // copies chunk c, this lane's token in pool row `row`, into stage c % NS
     auto issue = [&](int c, int32_t row) {
@@ -911,6 +938,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
         at = make_float4(fmaf(f, v.x, at.x), fmaf(f, v.y, at.y), fmaf(f, v.z, at.z),
                          fmaf(f, v.w, at.w));
       }
+      if (!a.dbg_part(p.pre, p.part + r)) continue;
       reinterpret_cast<float4*>(to_acc + (p.part + r) * D)[j] = at;
       if (j == 0) to_ml[p.part + r] = make_float2(mt, lt);
     }
@@ -938,7 +966,7 @@ __device__ __noinline__ bool row_is_finite(const PrefixArgs& a) {
   // the scales, a token to a lane (positions below 2^31 - 65536)
   for (int t = lane; __all_sync(0xffffffffu, ok) && t - lane < len; t += 32) {
     const int32_t* table = t < a.prefix_len ? a.prefix_table : a.block_table + int64_t(b) * a.max_pages;
-    const int64_t row = t < len ? a.map.row(table, uint32_t(t)) : -1;
+    const int64_t row = t < len ? a.pool_row(t < a.prefix_len, table, uint32_t(t)) : -1;
     if (row < 0) continue;
     const int64_t at = (row * a.heads + h) * ng;
     if (ng >= 8) {
@@ -995,7 +1023,7 @@ __device__ __noinline__ RowState<D / 64> attend_float32(const PrefixArgs& a) {
 #pragma unroll 1
   for (int t = 0; t < len; ++t) {
     const int32_t* table = t < a.prefix_len ? a.prefix_table : a.block_table + int64_t(b) * a.max_pages;
-    const int64_t row = a.map.row(table, uint32_t(t));
+    const int64_t row = a.pool_row(t < a.prefix_len, table, uint32_t(t));
     if (row < 0) continue;
     const int64_t vec = row * a.heads + h;
     float x = 0.0f;
@@ -1035,6 +1063,7 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
   const int g = a.q_per_kv, hq = a.heads * g;
   const int64_t v = merged_row<NW>();
   if (NW == 1 && v >= int64_t(a.n_seq) * hq) return;
+  if (!a.dbg_query(v)) return;   // the same in a block
   const int b = int(v / hq), h = int(v % hq) / g, j = int(v % hq) % g;
   const int64_t M = int64_t(a.n_seq) * g;
   const int n_pre = a.prefix_len > 0 && a.len(b) > 0 ? a.prefix_splits : 0;
@@ -1044,7 +1073,10 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
     return i < n_pre ? (int64_t(i) * a.heads + h) * M + int64_t(b) * g + j
                      : (int64_t(c0 + i - n_pre) * a.heads + h) * g + j;
   };
-  auto ml_of = [&](int i) { return (i < n_pre ? a.pre_ml : a.own_ml)[row_of(i)]; };
+  auto ml_of = [&](int i) {
+    return a.dbg_part(i < n_pre, row_of(i)) ? (i < n_pre ? a.pre_ml : a.own_ml)[row_of(i)]
+                                            : make_float2(-INFINITY, 0.0f);
+  };
   // a part without tokens has l = 0 (a NaN goes on)
   float m = -INFINITY;
   for (int i = NW == 1 ? lane : int(threadIdx.x); i < n; i += NW * 32) m = fmaxf(m, ml_of(i).x);
@@ -1070,6 +1102,7 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
 #pragma unroll 4
   for (int i = warp; i < n; i += NW) {
     const int64_t r = row_of(i);
+    if (!a.dbg_part(i < n_pre, r)) continue;
     const float2 ml = (i < n_pre ? a.pre_ml : a.own_ml)[r];
     const float2* src = reinterpret_cast<const float2*>((i < n_pre ? a.pre_acc : a.own_acc) + r * D);
     float2 x[E];

@@ -304,7 +304,9 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
     auto token = [&](int i, int k) { return t0 + i * TN + tr + k * RPP; };
     auto look_up = [&](int i, int k) {
       const int t = token(i, k);
-      return i < n && t < t1 ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t))) : -1;
+      return i < n && t < t1 && a.dbg_token(true, t)
+                 ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t)))
+                 : -1;
     };
     auto row_at = [&](int i, int k, int32_t p) {
       const uint32_t t = uint32_t(token(i, k));
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
         const uint16_t* sp = scales + vec * NG + pc * CC / G;
         w[k] = make_uint4(0, 0, 0, 0);
         s[k] = 0;
-        if (r[k] >= 0) {
+        if (r[k] >= 0 && a.dbg_row(r[k])) {
           w[k] = __ldg(reinterpret_cast<const uint4*>(codes + vec * CB) + pc);
           s[k] = GC == 2 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : uint32_t(__ldg(sp));
         }
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(PrefixMma<BITS, G, EXACT>::kThreads, 1)
       if (n > 0) (void)wait_or_abort(&vfull[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.guard);
       if (lim > *first_bad) l = NAN;
       const int64_t part = (int64_t(part_i) * a.heads + h) * M + r0 + r;
-      const bool live = r0 + r < M;
+      const bool live = r0 + r < M && a.dbg_part(true, part);
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         uint32_t o[32];

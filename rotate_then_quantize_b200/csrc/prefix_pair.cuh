@@ -237,7 +237,9 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int t = t0 + j * TN + lane + 32 * k;
-        page[k] = j < n && t < t1 ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t))) : -1;
+        page[k] = j < n && t < t1 && a.dbg_token(true, t)
+                      ? __ldg(a.prefix_table + a.map.page.div(uint32_t(t)))
+                      : -1;
       }
     };
     look_up(warp - 18);
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
         row[k] = uint32_t(page[k]) < uint32_t(a.map.n_pages)
                      ? int32_t(uint32_t(page[k]) * a.map.page.d + (t - a.map.page.div(t) * a.map.page.d))
                      : -1;
+        if (row[k] >= 0 && !a.dbg_row(row[k])) row[k] = -1;
       }
       look_up(j + 2);
       if (j >= NR && !__all_sync(0xffffffffu, wait_or_abort(&rempty[st], ((j / NR) & 1) ^ 1,
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(640, 1) prefix_pair_kernel(const PrefixArgs a)
         }
         if (lim > *first_bad) l = NAN;
         const int64_t part = (int64_t(SHARED ? part_i : 2 * part_i + u) * a.heads + h) * M + r0 + r;
-        const bool live = r0 + r < M;
+        const bool live = r0 + r < M && a.dbg_part(true, part);
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           uint32_t o[32];

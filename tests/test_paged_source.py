@@ -43,3 +43,29 @@ def test_workspace_is_not_read_through_the_read_only_path(name):
     for arg in _arguments(text, "__ldg"):
         used = set(re.findall(r"\w+", arg))
         assert not used & set(names), arg
+
+
+def _kernels(text):
+    """Name and body of every kernel."""
+    for m in re.finditer(r"__global__", text):
+        start = text.index("{", text.index(")", re.compile(r"\w+_kernel\(").search(text, m.end()).start()))
+        depth, i = 1, start + 1
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+        yield re.search(r"(\w+_kernel)\(", text[m.end():]).group(1), text[start:i]
+
+
+@pytest.mark.parametrize("name", CHAIN + ["launch_block_tables.cu"])
+def test_paged_kernels_check_their_indices(name):
+    """In the debug build every kernel checks the global indices that it computes."""
+    kernels = list(_kernels(_source(name)))
+    assert kernels
+    for kernel, body in kernels:
+        assert re.search(r"\bdbg_\w+\(|\bpool_row\(", body), kernel
+
+
+@pytest.mark.parametrize("name,calls", [("codec.cuh", 5), ("codec_split.cuh", 4)])
+def test_paged_codec_checks_its_slots(name, calls):
+    """The pool side of the paged codec: codes and scales, in and out."""
+    assert len(list(_arguments(_source(name), "dbg_slot"))) >= calls
