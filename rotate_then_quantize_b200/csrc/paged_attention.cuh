@@ -1053,11 +1053,12 @@ __device__ __noinline__ RowState<D / 64> attend_float32(const PrefixArgs& a) {
 // the warps in order; the rotation by the first warp.
 template <int ROT, int D, int NW>
 __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
-                                  NW == 16 ? (D == 256 ? 1 : 2) : (D == 256 ? 5 : 8))
+                                  NW == 1 && D == 256 ? 5 : NW == 16 ? 2 : 8)
     prefix_merge_kernel(const __grid_constant__ PrefixArgs a) {
   constexpr int E = D / 64;
   __shared__ float acc_sh[NW][D];
   __shared__ float2 ml_sh[NW];
+  __shared__ __align__(16) float end_sh[NW == 1 ? 4 : D + D / 4];   // lambda, signs
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : int(threadIdx.x >> 5);
   const int g = a.q_per_kv, hq = a.heads * g;
@@ -1066,6 +1067,12 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
   if (!a.dbg_query(v)) return;   // the same in a block
   const int b = int(v / hq), h = int(v % hq) / g, j = int(v % hq) % g;
   const int64_t M = int64_t(a.n_seq) * g;
+  if constexpr (NW > 1) {
+    const int i = int(threadIdx.x);
+    if (i < D / 4) copy16(smem_addr(end_sh + 4 * i), a.v_lambda + int64_t(h) * D + 4 * i, true);
+    else if (i < D / 4 + D / 16)
+      copy16(smem_addr(end_sh + D + 4 * (i - D / 4)), a.v_signs + int64_t(h) * D + 16 * (i - D / 4), true);
+  }
   const int n_pre = a.prefix_len > 0 && a.len(b) > 0 ? a.prefix_splits : 0;
   const int c0 = a.chunk_start[b], n = n_pre + a.chunk_start[b + 1] - c0;
   // parts 0 .. n_pre - 1 of the prefix, then the sequence's own
@@ -1120,6 +1127,7 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
     if (lane == 0) ml_sh[warp].y = l;
 #pragma unroll
     for (int e = 0; e < E; ++e) reinterpret_cast<float2*>(acc_sh[warp])[lane + 32 * e] = acc[e];
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (warp > 0) return;
     l = 0.0f;
@@ -1135,14 +1143,17 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
       }
     }
   }
-  // on their way before the call below, which nothing is moved across
+  // lambda and signs: on their way before the calls below, which nothing is moved
+  // across; from shared memory they need no registers over them
   float2 lam[E];
   int8_t sg[2 * E];
+  if constexpr (NW == 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    lam[e] = reinterpret_cast<const float2*>(a.v_lambda + int64_t(h) * D)[warp_pair<ROT, D>(lane, e)];
-    sg[2 * e] = a.v_signs[int64_t(h) * D + 2 * (E * lane + e)];
-    sg[2 * e + 1] = a.v_signs[int64_t(h) * D + 2 * (E * lane + e) + 1];
+    for (int e = 0; e < E; ++e) {
+      lam[e] = reinterpret_cast<const float2*>(a.v_lambda + int64_t(h) * D)[warp_pair<ROT, D>(lane, e)];
+      sg[2 * e] = a.v_signs[int64_t(h) * D + 2 * (E * lane + e)];
+      sg[2 * e + 1] = a.v_signs[int64_t(h) * D + 2 * (E * lane + e) + 1];
+    }
   }
   bool finite = fabsf(l) < INFINITY;
 #pragma unroll
@@ -1156,6 +1167,14 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
       l = s.l;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = s.acc[e];
+    }
+  }
+  if constexpr (NW > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      lam[e] = reinterpret_cast<const float2*>(end_sh)[warp_pair<ROT, D>(lane, e)];
+      sg[2 * e] = reinterpret_cast<const int8_t*>(end_sh + D)[2 * (E * lane + e)];
+      sg[2 * e + 1] = reinterpret_cast<const int8_t*>(end_sh + D)[2 * (E * lane + e) + 1];
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : l;   // no token: 0 (a NaN stays)
