@@ -389,6 +389,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t pack_half2_away(float lo, float hi) {
+  const __half2 h = __halves2half2(lo < 0.0f ? __float2half_rd(lo) : __float2half_ru(lo),
+                                   hi < 0.0f ? __float2half_rd(hi) : __float2half_ru(hi));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ float2 unpack_half2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
@@ -625,7 +630,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
       if (t == 0) qsum[8 * s + g] = sum;
     }
     __syncthreads();
-    // offsets of groups 2t, 2t + 1 (+ 8 o) as fp16 hi and lo: -(8 or 128) 2^-24 sum q
+    // offsets of groups 2t, 2t + 1 (+ 8 o) as fp16 hi and lo: -(8 or 128) 2^-24 sum q.
+    // hi is rounded away from zero, so lo has the other sign or is zero: an infinite
+    // scale of keys then makes the score NaN, never the -inf of a token not attended to
     constexpr int NO = NG > 8 ? NG / 8 : 1;
     uint32_t off[NO][2];
 #pragma unroll
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
         }
         x[k] *= BITS == 4 ? -0x1p-21f : -0x1p-17f;
       }
-      off[o][0] = pack_half2(x[0], x[1]);
+      off[o][0] = pack_half2_away(x[0], x[1]);
       off[o][1] = half2_rest(x[0], x[1], off[o][0]);
     }
     // columns 2t and 2t + 1 of the score tile: their factor, token limit

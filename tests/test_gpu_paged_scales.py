@@ -137,3 +137,25 @@ def test_nothing_stays_from_a_call_with_large_scales(n_seq, prefix, d, dtype):
         lam.copy_(x["v_lambda"])
         graph.replay()
         assert torch.equal(out, want[(1, 0, 1)[i]])
+
+
+@pytest.mark.parametrize("n_seq,prefix,d,dtype", KERNELS + [(40, 0, 128, "float16"),
+                                                            (40, 0, 64, "bfloat16")])
+@pytest.mark.parametrize("bits,group", [(4, 16), (8, 64)])
+def test_infinite_key_scale(n_seq, prefix, d, dtype, bits, group):
+    """An infinite scale of keys makes NaN of every query head that attends to its
+    token, whatever the signs of its codes and query; a score of -inf would leave
+    the token out without a word."""
+    _, q, dev, host = _case(n_seq, prefix, d, dtype, bits, group, seed=7)
+    want = rq.prefix_attention(q, **dev)
+    table, t = (host["prefix_table"], 3) if prefix else (host["block_table"][0], 3)
+    row = int(paged.rows_of(table, np.array([t]), 16, 10 ** 9)[0])
+    ng = d // group
+    for g, value in ((0, np.inf), (ng - 1, -np.inf)):
+        scales = dev["k_scales"].clone()
+        scales[row, 1, g] = value
+        got = rq.prefix_attention(q, **{**dev, "k_scales": scales})
+        hit = _t(host["seq_lens"] > t) if prefix else _t(np.arange(n_seq) == 0)
+        assert bool(got[hit][:, 4:].isnan().all())
+        assert bool((got[:, :4] == want[:, :4]).all()) and bool((got[~hit] == want[~hit]).all())
+    assert rq.srftq_check_device() == 0
