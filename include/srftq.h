@@ -393,8 +393,14 @@ int srftq_dequantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_r
  *                aligned, written; calls that may run at the same time need
  *                one each. Nothing in it is kept from one call to the next.
  *
- * The parts' softmax states are kept in float32 and joined in a fixed order:
- * the result does not depend on scheduling. Three launches, four with many
+ * Arithmetic: rotations, scores' sums, softmax states and values' sums are
+ * float32, and parts are joined in a fixed order: the result does not depend on
+ * scheduling. Rounded to fewer bits are, for either dtype, the products of scale
+ * and code of the values, once to fp16 (11 bits, for every size of the scales);
+ * for bf16 outputs also the rotated query and the softmax weights (fp16), and,
+ * for batches with many query rows, the products of scale and code of the keys;
+ * for fp16 outputs these three are held as an fp16 value and its rest, 22 bits.
+ * (srftq_decode_attention keeps values in float32.) Three launches, four with many
  * query rows per KV head, no copy to the host: lengths and tables may come from
  * calls before it on the stream.
  */

@@ -10,14 +10,33 @@ namespace srftq {
 // KV head whatever their number, the warp-level one 8 at a time, so its time per
 // token grows with the rows and breaks even at kEvenRows of each 128; a launch
 // more, the query tiles and a block's start cost the others 5 us, which the rows
-// beyond must win back over all tokens and heads. One B200, int4, fp16 / bf16, us
-// a call, warp-level against tcgen05:
+// beyond must win back over all tokens and heads. Both fit int4 with 8 heads of d =
+// 128 and 4 of 256; elsewhere the rule is off by up to a fifth next to its border,
+// for int8 at d = 256 by a third. One B200, fp16 / bf16, us a call, warp-level
+// against tcgen05 (* where the rule takes the slower one). int4:
 //   28672 tokens, 8 heads of d = 128: 16 rows 49 : 55 / 44 : 46, 24 rows 63 : 55 /
 //     53 : 46, 32 rows 75 : 55 / 65 : 45, 64 rows 126 : 59 / 110 : 49;
 //   28672 tokens, 4 heads of d = 256: 24 rows 69 : 104 / 61 : 69, 32 rows 83 : 103 /
 //     73 : 68, 48 rows 108 : 104 / 92 : 69;
 //   6000 tokens, d = 128: 24 rows 32 : 36 / 29 : 32, 32 rows 36 : 36 / 33 : 31;
-//   1024 tokens, d = 128: 32 rows 25 : 30 / 25 : 28, 48 rows 27 : 31 / 26 : 29.
+//   1024 tokens, d = 128: 32 rows 25 : 30 / 25 : 28, 48 rows 27 : 31 / 26 : 29;
+//   28672 tokens, 8 heads of d = 64: 16 rows 35 : 45 / 33 : 38, 24 rows 45 : 45 /
+//     41 : 38, 32 rows 54 : 45 / 49 : 37; 6000 tokens: 32 rows 25 : 29 / 23 : 25,
+//     48 rows 29 : 31* / 27 : 29*, 64 rows 33 : 31 / 31 : 29;
+//   28672 tokens, 2 heads of d = 128: 24 rows 31 : 38 / 29 : 33, 32 rows 33 : 38* /
+//     31 : 33*, 48 rows 39 : 39 / 35 : 35, 64 rows 45 : 39 / 40 : 35; 1 head: 48 rows
+//     31 : 37* / 29 : 33*, 64 rows 33 : 38* / 29 : 34*, 96 rows 38 : 39 / 35 : 35;
+//   120000 tokens, 2 heads of d = 128: 16 rows 47 : 58 / 43 : 48, 24 rows 62 : 60 /
+//     54 : 50, 32 rows 72 : 59 / 64 : 49;
+//   28672 tokens, 1 head of d = 256: 64 rows 57 : 66 / 51 : 50, 96 rows 65 : 68* /
+//     58 : 51.
+// int8:
+//   28672 tokens, 8 heads of d = 128: 16 rows 58 : 60 / 50 : 47*, 24 rows 74 : 62 /
+//     63 : 48; 4096 tokens: 32 rows 30 : 33 / 28 : 29, 48 rows 38 : 35 / 35 : 33;
+//   28672 tokens, 2 heads of d = 128: 24 rows 37 : 39 / 33 : 33, 32 rows 41 : 39 /
+//     37 : 33;
+//   28672 tokens, 4 heads of d = 256: 24 rows 96 : 108 / 85 : 78*, 32 rows 119 : 110* /
+//     102 : 78*, 48 rows 160 : 118* / 134 : 83, 64 rows 197 : 116 / 165 : 85.
 constexpr int64_t kMmaGain = 3 << 18;   // (rows beyond) x tokens x heads
 constexpr int64_t even_rows(int32_t d, bool exact) { return d <= 128 ? 16 : exact ? 46 : 30; }
 

@@ -46,15 +46,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // first chunk of every sequence (chunk c of sequence b covers the own tokens
 // [c chunk, (c + 1) chunk)).
 struct PrefixPlan {
-  int32_t chunk;      // tokens per chunk, a multiple of 128
   int32_t n_chunks;   // chunks of all sequences
   int32_t taken;      // items that blocks have taken beyond their first
-  int32_t pad;
 };
 
 struct PrefixArgs {
   int32_t n_seq, heads, q_per_kv, lg_group;
-  int32_t prefix_len, max_pages, max_chunks;
+  int32_t prefix_len, max_pages;
   int32_t prefix_splits, prefix_per;   // parts of the prefix and tokens of each
   int32_t chunk_goal;                  // chunks that the plan aims for
   PageMap map;
@@ -193,7 +191,6 @@ __device__ inline void plan_own_tokens(const PrefixArgs& a) {
   }
   if (tid == 0) {
     a.chunk_start[a.n_seq] = carry;
-    a.plan->chunk = chunk;
     a.plan->n_chunks = carry;
     a.plan->taken = 0;
   }
@@ -312,8 +309,10 @@ __global__ void __launch_bounds__(256) prefix_prepare_kernel(const PrefixArgs a)
 // more product, of the scales (fp16, exact) with -8 2^-24 sum_{j in G} q_j. The
 // query is scaled by a power of two to [2^13, 2^14) and held as fp16 hi (+ lo
 // when the output is fp16). The scale multiplies D_G in float32, so a score's
-// only rounding to fewer bits is the query's: 2^-12 for bf16 outputs (whose own
-// step is 2^-9), 2^-23 for fp16.
+// roundings to fewer bits are the query's, 2^-12 for bf16 outputs (whose own
+// step is 2^-9), 2^-23 for fp16, and the offset's: its lo ends at fp16's last
+// subnormal bit, half a step of which is half of c q at q = 1, where q is up to
+// 2^14: 2^-17 of a score's standard deviation over 8 groups of 16 int4 codes.
 //
 // Values, O[coord][query] += sum_t (sigma c)[coord][t] p'[t][query], p' =
 // 2^7 e^{x - m}, m a reference that follows the maximum when that grows by more
