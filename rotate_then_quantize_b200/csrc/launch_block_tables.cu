@@ -168,8 +168,9 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TableAr
 int launch_block_tables(const BlockTablesCall& c) {
   TableArgs a{int32_t(c.n_seq), c.cached_lens, c.new_lens, FastDiv::make(uint32_t(c.page_size)),
               c.free_pages,     c.n_free,      c.block_table, int32_t(c.max_pages), c.slots,
-              c.n_slots,        c.seq_lens,    c.row_start,   c.counts, Runtime::guard_word()};
-  if (!a.guard) return SRFTQ_ERR_CUDA;
+              c.n_slots,        c.seq_lens,    c.row_start,   c.counts,
+              kDebugChecks ? Runtime::guard_word() : nullptr};
+  if (kDebugChecks && !a.guard) return SRFTQ_ERR_CUDA;
   // a block for each 1024 slots, up to two per SM (each scans all lengths)
   const int64_t want = (c.n_slots + kTabThreads - 1) / kTabThreads;
   const int64_t cap = 2 * int64_t(Runtime::num_sms());

@@ -854,8 +854,9 @@ __global__ void __launch_bounds__(kTileWarps * 32, D == 256 ? 2 : D == 128 ? 4 :
           if constexpr (EXACT) mma_f16(O[s], a0, a1, a2, a3, pl[mt][0], pl[mt][1]);
         };
         // fp16 1024 + u, or 1024 + 16 u, to c (exact)
-        constexpr uint32_t k1 = 0x3C003C00u, k16 = 0x2C002C00u;                   // 1, 2^-4
-        constexpr uint32_t o8 = 0xE408E408u, o72 = 0xD480D480u, o128 = 0xE480E480u;   // -1032, -72, -1152
+        constexpr uint32_t k1 = 0x3C003C00u, k16 = 0x2C002C00u;   // 1, 2^-4
+        // -1032, -72, -1152
+        constexpr uint32_t o8 = 0xE408E408u, o72 = 0xD480D480u, o128 = 0xE480E480u;
         if constexpr (BITS == 4) {
 #pragma unroll
           for (int s = 0; s < S16; s += 2) {
@@ -1077,7 +1078,8 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32,
     const int i = int(threadIdx.x);
     if (i < D / 4) copy16(smem_addr(end_sh + 4 * i), a.v_lambda + int64_t(h) * D + 4 * i, true);
     else if (i < D / 4 + D / 16)
-      copy16(smem_addr(end_sh + D + 4 * (i - D / 4)), a.v_signs + int64_t(h) * D + 16 * (i - D / 4), true);
+      copy16(smem_addr(end_sh + D + 4 * (i - D / 4)),
+             a.v_signs + int64_t(h) * D + 16 * (i - D / 4), true);
   }
   const int n_pre = a.prefix_len > 0 && a.len(b) > 0 ? a.prefix_splits : 0;
   const int c0 = a.chunk_start[b], n = n_pre + a.chunk_start[b + 1] - c0;

@@ -7,11 +7,12 @@
 //   P[row][token]  = 2^7 e^{x - ref}, fp16, written over S in tensor memory;
 //   O[row][coord] += P (sigma c)              P from tensor memory.
 // Warps 4-7 turn packed codes into swizzled fp16 tiles (sigma c, rounded once:
-// kLargeScale), warp 8 issues the products, warps 0-3 hold a query row per thread: its maximum and sum need no exchange.
-// Two score buffers let the tensor cores form the next scores while the
-// exponentials of these are taken. O is rescaled only when a row's maximum
-// grows by more than 2^8 over the reference its weights use (the weights then
-// stay below 2^15 in fp16; the final quotient does not see the reference).
+// kLargeScale), warp 8 issues the products, warps 0-3 hold a query row per thread:
+// its maximum and sum need no exchange. Two score buffers let the tensor cores
+// form the next scores while the exponentials of these are taken. O is rescaled
+// only when a row's maximum grows by more than 2^8 over the reference its weights
+// use (the weights then stay below 2^15 in fp16; the final quotient does not see
+// the reference).
 //
 // The query row is scaled by a power of two to [2^13, 2^14) and rounded to
 // fp16. For fp16 outputs (EXACT) that is not enough: queries, keys and weights

@@ -34,7 +34,7 @@
 // What it reaches is the chain of a tile: decode, scores, exponentials, values,
 // each handed on through a barrier. 128 sequences x 8 queries x 8 heads of d = 128
 // over 32768 int4 tokens, bf16: 168 us, against 80 of the products at the measured
-// dense rate. 16 x 8 x 8 over 131072 int8 tokens: 138 us the whole call, 39 of
+// dense rate. 16 x 8 x 8 over 131072 int8 tokens: 141 us the whole call, 39 of
 // products, 47 of memory; without the decoding of the two int8 tiles it took 43
 // less. On a small case ncu shows 28 % of the tensor pipe, 29 % of the special
 // function units and 36 % of the issue slots.
