@@ -379,8 +379,11 @@ int srftq_dequantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_r
  * zeros. A sequence may be shorter than the prefix. A token whose table entry
  * is no page of the pool (negative, n_pages or more) is left out. What lies in
  * the pool behind a sequence's last token is never used, whatever it holds; a
- * scale that is not finite reaches the sequences that attend to its token only,
- * among the shared tokens too.
+ * scale that is not finite makes NaN of the query heads that attend to its token,
+ * and of no others, among the shared tokens too. Scales of 8192 (int4) or 512
+ * (int8) and more, which only vectors next to fp16's end have, give the right
+ * result, but a query head that attends to one may be done by one warp, a token
+ * at a time: far slower, 1 us a token.
  *
  *   q            [n_seq][heads*q_per_kv][d], out alike: fp16 or bf16 (dtype)
  *   k_codes, v_codes, k_scales, v_scales: pools of n_pages*page_size rows
@@ -400,9 +403,10 @@ int srftq_dequantize_paged(const srftq_desc* desc, int64_t n_slices, int64_t n_r
  * for bf16 outputs also the rotated query and the softmax weights (fp16), and,
  * for batches with many query rows, the products of scale and code of the keys;
  * for fp16 outputs these three are held as an fp16 value and its rest, 22 bits.
- * (srftq_decode_attention keeps values in float32.) Three launches, four with many
- * query rows per KV head, no copy to the host: lengths and tables may come from
- * calls before it on the stream.
+ * (srftq_decode_attention keeps values in float32.)
+ *
+ * Three launches, four with many query rows per KV head, no copy to the host:
+ * lengths and tables may come from calls before it on the stream.
  */
 int srftq_prefix_attention(const srftq_desc* desc, int32_t dtype, int64_t n_seq, int32_t q_per_kv,
                            const void* q, const uint8_t* k_codes, const uint16_t* k_scales,
